@@ -328,8 +328,9 @@ def _plain_kept(v):
     rows, f = v.shape
     p = torch.nn.functional.pad(v, (0, -f % 128)).view(rows, -1, 128)
     a = p.abs().amax(-1, keepdim=True).clamp(min=1e-4)
-    q = (p * (448.0 / a)).clamp(-448.0, 448.0).to(torch.float8_e4m3fn).float()
-    return (q * (a / 448.0)).view(rows, -1)[:, :f]
+    most = torch.full_like(a, 448.0)  # a tensor: quotients by a number are not rounded once on every device
+    q = (p * (most / a)).clamp(-448.0, 448.0).to(torch.float8_e4m3fn).float()
+    return (q * (a / most)).view(rows, -1)[:, :f]
 
 
 def _plain_glu(gate, up, grad=None):
@@ -450,9 +451,10 @@ def _exact_kept(v):
     for lo in range(0, v.shape[1], 128):
         part = v[:, lo:lo + 128]
         a = part.abs().amax(1, keepdim=True).float().clamp(min=1e-4)
-        m = (part.float() * (448.0 / a)).double()  # the format's rule: both quotients and the product in 32 bits
+        most = torch.full_like(a, 448.0)
+        m = (part.float() * (most / a)).double()  # the format's rule: both quotients and the product in 32 bits
         step = torch.exp2(torch.floor(torch.log2(m.abs().clamp(min=2.0 ** -6))) - 3)
-        out[:, lo:lo + 128] = torch.round(m / step).mul(step).clamp(-448.0, 448.0) * (a / 448.0).double()
+        out[:, lo:lo + 128] = torch.round(m / step).mul(step).clamp(-448.0, 448.0) * (a / most).double()
     return out
 
 

@@ -699,6 +699,8 @@ void set_wait_limit_ns(uint64_t ns) {
   g_wait_limit_ns.store(ns == 0 || ns > kWaitLimitNs ? kWaitLimitNs : ns, std::memory_order_relaxed);
 }
 
+uint64_t wait_limit_ns() { return g_wait_limit_ns.load(std::memory_order_relaxed); }
+
 int read_device_status(int32_t* out, bool clear) {
   int v = 0;
   if (cudaMemcpyFromSymbol(&v, g_device_status, sizeof(int)) != cudaSuccess) {
@@ -712,8 +714,10 @@ int read_device_status(int32_t* out, bool clear) {
       return MOE_ERR_CUDA;
     }
   }
-  *out = v;
-  return MOE_OK;
+  int32_t ve = 0;  // the experts' kernels keep a word of their own
+  const int rc = read_expert_status(&ve, clear);
+  *out = v != 0 ? v : ve;
+  return rc;
 }
 
 cudaError_t launch_combine_ranks(const uint8_t* partials, uint8_t* out, int64_t rows,

@@ -132,6 +132,45 @@ struct RankCombineBwdParams {
   int num_tokens, num_ranks, hidden_size;
 };
 
+struct RouteParams {
+  const void* logits;       // fp32 or bf16 [N, stride]
+  const float* bias;        // [E] or null
+  int32_t* topk_idx;        // [N, k]
+  float* topk_weights;      // [N, k]
+  const float* grad_weights;  // backward: [N, k]
+  void* grad_logits;          // backward: [N, E], the logits' kind
+  int64_t stride;
+  int num_tokens, num_experts, topk, num_groups, topk_groups;
+  int score, group_score, renormalize, logits_kind;
+  float scale;
+};
+
+struct GluParams {
+  const int32_t* num_rows;  // device row count, or null
+  const uint8_t* gate_up;   // bf16 [rows, 2F] (forward)
+  uint8_t* act;             // bf16 [rows, F], may be null
+  uint8_t* ckpt;            // e4m3 [rows, 2F] (forward: may be null)
+  float* scales;            // fp32 [rows, 2 * ceil(F / 128)]
+  const uint8_t* grad_act;  // backward: bf16 [rows, F]
+  uint8_t* grad_gate_up;    // backward: bf16 [rows, 2F]
+  int64_t rows;
+  int width;
+};
+
+struct ExpertParams {
+  const int32_t* row_begin;  // [E]
+  const int32_t* row_end;    // [E]
+  const uint8_t* x;          // bf16 rows: x, or grad_y
+  const uint8_t* x2;         // weight gradient: the rows of x
+  const uint8_t* w;          // bf16 [E, N, K]
+  uint8_t* out;              // y, act, grad_x or grad_w
+  uint8_t* ckpt;             // moe_expert_swiglu: e4m3 [rows, 2F], or null
+  float* scales;
+  int64_t rows, x_stride;    // x_stride: elements between rows of x
+  int num_experts, in_features, out_features;
+  int grad_kind;             // MOE_GRAD_*
+};
+
 // Programmatic dependent launch. Every kernel of this library begins with
 // pdl_wait() -- griddepcontrol.wait: until the previous kernel in the stream
 // has completed and its memory operations are visible -- before its first
@@ -186,6 +225,9 @@ int read_device_status(int32_t* out, bool clear);
 // The budget of the bounded waits for launches from now on (ns; 0 = the
 // default kWaitLimitNs; clamped to it).
 void set_wait_limit_ns(uint64_t ns);
+uint64_t wait_limit_ns();
+// The experts' kernels' part of read_device_status.
+int read_expert_status(int32_t* out, bool clear);
 cudaError_t launch_slots(bool pack, const void* const* src, void* const* dst,
                          const moe_slot_desc_t* d, const int64_t* offsets, int64_t slot_bytes,
                          cudaStream_t s);
@@ -210,6 +252,14 @@ cudaError_t launch_dispatch_packed(const DispatchParams& p, int out_kind, uint8_
 cudaError_t launch_mask_topk_ids(int32_t* ids, int64_t total, int topk, const int32_t* num_actual,
                                  cudaStream_t s);
 constexpr int kMaxHiddenNorm = 16384;
+cudaError_t launch_route(const RouteParams& p, cudaStream_t s);
+cudaError_t launch_route_backward(const RouteParams& p, cudaStream_t s);
+cudaError_t launch_swiglu(const GluParams& p, cudaStream_t s);
+cudaError_t launch_swiglu_backward(const GluParams& p, cudaStream_t s);
+cudaError_t launch_expert_product(const ExpertParams& p, cudaStream_t s);
+cudaError_t launch_expert_swiglu(const ExpertParams& p, cudaStream_t s);
+cudaError_t launch_expert_grad_input(const ExpertParams& p, cudaStream_t s);
+cudaError_t launch_expert_grad_weight(const ExpertParams& p, cudaStream_t s);
 
 #ifdef __CUDACC__
 
@@ -392,6 +442,19 @@ __device__ __forceinline__ void bulk_g2s(void* sdst, const void* gsrc, uint32_t 
           smem_u32(sdst)),
       "l"(gsrc), "r"(bytes), "r"(smem_u32(bar)), "l"(pol)
       : "memory");
+}
+
+// sigmoid(g) and 1 - sigmoid(g) from e = exp(-|g|), which cannot overflow: the
+// smaller of the two is e / (1 + e), with its leading digits, however large |g|.
+__device__ __forceinline__ void sigmoid_pair(float g, float& sig, float& rest) {
+  const float e = __expf(-fabsf(g)), r = __fdividef(1.0f, 1.0f + e), s = e * r;
+  sig = g >= 0.0f ? r : s;
+  rest = g >= 0.0f ? s : r;
+}
+__device__ __forceinline__ float swiglu_of(float g, float u) {
+  float sig, rest;
+  sigmoid_pair(g, sig, rest);
+  return g * sig * u;
 }
 
 // Inclusive warp scan of an int.

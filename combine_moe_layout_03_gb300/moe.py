@@ -37,6 +37,17 @@ MOE_COMBINE_TOPK = 0
 MOE_COMBINE_RANKS = 1
 MOE_COMBINE_TOPK_RANKS = 2
 
+MOE_SCORE_SOFTMAX = 0
+MOE_SCORE_SIGMOID = 1
+MOE_GROUP_MAX = 0
+MOE_GROUP_TOP2_SUM = 1
+MOE_LOGITS_F32 = 0
+MOE_LOGITS_BF16 = 1
+
+MOE_GRAD_BF16 = 0
+MOE_GRAD_F32 = 1
+MOE_GRAD_F32_ADD = 2
+
 if not os.path.exists(LIB_PATH):
     raise ImportError(
         f"{LIB_PATH} is missing: build it with `python -c \"import __graft_entry__ as g; g.build()\"` "
@@ -125,6 +136,31 @@ _lib.moe_pack_record.restype = ctypes.c_int
 _lib.moe_pack_record.argtypes = [_D, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _vp]
 _lib.moe_unpack_record.restype = ctypes.c_int
 _lib.moe_unpack_record.argtypes = [_D, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]
+
+
+class _RouteDesc(ctypes.Structure):
+    _fields_ = [(name, _i32) for name in ("num_tokens", "num_experts", "topk", "num_groups", "topk_groups", "score",
+                                          "group_score", "renormalize", "logits_kind", "logits_stride")]
+    _fields_ += [("scale", ctypes.c_float)]
+
+
+class _GluDesc(ctypes.Structure):
+    _fields_ = [("rows", _i64), ("width", _i32)]
+
+
+class _ExpertDesc(ctypes.Structure):
+    _fields_ = [("rows", _i64), ("x_stride", _i64), ("num_experts", _i32), ("in_features", _i32),
+                ("out_features", _i32)]
+
+
+for _name, _desc, _args in (
+        ("moe_route", _RouteDesc, [_vp] * 5), ("moe_route_backward", _RouteDesc, [_vp] * 5),
+        ("moe_swiglu", _GluDesc, [_vp] * 6), ("moe_swiglu_backward", _GluDesc, [_vp] * 7),
+        ("moe_expert_product", _ExpertDesc, [_vp] * 6), ("moe_expert_swiglu", _ExpertDesc, [_vp] * 8),
+        ("moe_expert_product_backward_input", _ExpertDesc, [_vp] * 6),
+        ("moe_expert_product_backward_weight", _ExpertDesc, [_vp] * 5 + [ctypes.c_int, _vp])):
+    getattr(_lib, _name).restype = ctypes.c_int
+    getattr(_lib, _name).argtypes = [ctypes.POINTER(_desc)] + _args
 
 
 class MoeError(RuntimeError):
@@ -779,6 +815,295 @@ def prepare_combine_norm(desc: MoeDesc, mode: int, expert_out, topk_idx, topk_we
                                                residual_in, gamma, normed_out, residual_out))
 
 
+# ---- router, gated activation and experts' products ---------------------------
+# The descriptors hold sizes and kinds; what a call reads and writes is checked
+# against them here (type, device, density and room), since the library sees
+# pointers only.
+
+@dataclass
+class MoeRouteDesc:
+    """Shape and rule of one router call (moe_route_desc_t)."""
+    num_tokens: int
+    num_experts: int
+    topk: int
+    score: int = MOE_SCORE_SOFTMAX
+    num_groups: int = 1
+    topk_groups: int = 1
+    group_score: int = MOE_GROUP_TOP2_SUM
+    renormalize: bool = True
+    scale: float = 1.0
+    logits_kind: int = MOE_LOGITS_F32
+    logits_stride: int = 0
+
+    def c(self) -> _RouteDesc:
+        return _RouteDesc(self.num_tokens, self.num_experts, self.topk, self.num_groups, self.topk_groups, self.score,
+                          self.group_score, int(self.renormalize), self.logits_kind, self.logits_stride, self.scale)
+
+    @property
+    def logits_dtype(self):
+        return torch.bfloat16 if self.logits_kind == MOE_LOGITS_BF16 else torch.float32
+
+
+@dataclass
+class MoeGluDesc:
+    """Rows and width F of one gated activation (moe_glu_desc_t)."""
+    rows: int
+    width: int
+
+    def c(self) -> _GluDesc:
+        return _GluDesc(self.rows, self.width)
+
+    @property
+    def groups(self) -> int:
+        return -(-self.width // 128)
+
+
+@dataclass
+class MoeExpertDesc:
+    """Shape of one call of the experts' products (moe_expert_desc_t)."""
+    num_experts: int
+    rows: int
+    in_features: int
+    out_features: int
+    x_stride: int = 0
+
+    def c(self) -> _ExpertDesc:
+        return _ExpertDesc(self.rows, self.x_stride, self.num_experts, self.in_features, self.out_features)
+
+
+def _want(what: str, t, dtype, numel: int, optional: bool = False):
+    """t is a dense CUDA tensor of dtype with at least numel elements."""
+    if t is None:
+        if optional or numel <= 0:
+            return
+        raise MoeError(MOE_ERR_INVALID_ARG, f"{what}: missing")
+    if t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
+        raise MoeError(MOE_ERR_INVALID_ARG, f"{what}: a dense CUDA tensor of {dtype} is wanted")
+    if t.numel() < numel:
+        raise MoeError(MOE_ERR_CAPACITY, f"{what}: {t.numel()} elements, {numel} needed")
+
+
+def _want_rows(what: str, t, rows: int, width: int, stride: int):
+    """t is a bf16 CUDA tensor holding `rows` rows of `width` elements, `stride` apart."""
+    if t is None:
+        if rows <= 0:
+            return
+        raise MoeError(MOE_ERR_INVALID_ARG, f"{what}: missing")
+    if t.dtype != torch.bfloat16 or not t.is_cuda or (t.dim() and t.numel() and t.stride(-1) != 1):
+        raise MoeError(MOE_ERR_INVALID_ARG, f"{what}: a bf16 CUDA tensor with dense rows is wanted")
+    have = t.untyped_storage().nbytes() // 2 - t.storage_offset()
+    if rows > 0 and have < (rows - 1) * stride + width:
+        raise MoeError(MOE_ERR_CAPACITY, f"{what}: {have} elements, {(rows - 1) * stride + width} needed")
+    if t.dim() == 2 and t.shape[0] > 1 and t.stride(0) != stride:
+        raise MoeError(MOE_ERR_INVALID_ARG, f"{what}: rows are {t.stride(0)} elements apart, the descriptor says {stride}")
+
+
+def _want_logits(desc: MoeRouteDesc, logits):
+    n, e = desc.num_tokens, desc.num_experts
+    stride = desc.logits_stride or e
+    if logits is None:
+        _want("logits", None, desc.logits_dtype, n * e)
+        return
+    if logits.dtype != desc.logits_dtype or not logits.is_cuda or (logits.numel() and logits.stride(-1) != 1):
+        raise MoeError(MOE_ERR_INVALID_ARG, f"logits: a CUDA tensor of {desc.logits_dtype} with dense rows is wanted")
+    have = logits.untyped_storage().nbytes() // logits.element_size() - logits.storage_offset()
+    if n > 0 and have < (n - 1) * stride + e:
+        raise MoeError(MOE_ERR_CAPACITY, f"logits: {have} elements, {(n - 1) * stride + e} needed")
+    if logits.dim() == 2 and logits.shape[0] > 1 and logits.stride(0) != stride:
+        raise MoeError(MOE_ERR_INVALID_ARG,
+                       f"logits: rows are {logits.stride(0)} elements apart, the descriptor says {stride}")
+
+
+def prepare_route(desc: MoeRouteDesc, logits, bias, topk_idx, topk_weights, stream=None) -> Prepared:
+    n, k = desc.num_tokens, desc.topk
+    _want_logits(desc, logits)
+    _want("bias", bias, torch.float32, desc.num_experts, optional=True)
+    _want("topk_idx", topk_idx, torch.int32, n * k)
+    _want("topk_weights", topk_weights, torch.float32, n * k)
+    d = desc.c()
+    args = (ctypes.byref(d), *_vps(logits, bias, topk_idx, topk_weights), ctypes.c_void_p(_stream(stream)))
+    return Prepared("moe_route", args, (d, logits, bias, topk_idx, topk_weights))
+
+
+def moe_route(desc: MoeRouteDesc, logits, bias=None, topk_idx=None, topk_weights=None, stream=None):
+    """The experts of each token and their weights (see include/moe.h).
+    Returns (topk_idx int32 [N, k], topk_weights fp32 [N, k])."""
+    shape = (desc.num_tokens, desc.topk)
+    if topk_idx is None:
+        topk_idx = torch.empty(shape, dtype=torch.int32, device=logits.device)
+    if topk_weights is None:
+        topk_weights = torch.empty(shape, dtype=torch.float32, device=logits.device)
+    prepare_route(desc, logits, bias, topk_idx, topk_weights, stream)()
+    return topk_idx, topk_weights
+
+
+def prepare_route_backward(desc: MoeRouteDesc, logits, topk_idx, grad_weights, grad_logits, stream=None) -> Prepared:
+    n, k = desc.num_tokens, desc.topk
+    _want_logits(desc, logits)
+    _want("topk_idx", topk_idx, torch.int32, n * k)
+    _want("grad_weights", grad_weights, torch.float32, n * k)
+    _want("grad_logits", grad_logits, desc.logits_dtype, n * desc.num_experts)
+    d = desc.c()
+    args = (ctypes.byref(d), *_vps(logits, topk_idx, grad_weights, grad_logits), ctypes.c_void_p(_stream(stream)))
+    return Prepared("moe_route_backward", args, (d, logits, topk_idx, grad_weights, grad_logits))
+
+
+def moe_route_backward(desc: MoeRouteDesc, logits, topk_idx, grad_weights, grad_logits=None, stream=None):
+    """Gradient of the logits, [N, E] of their type (see include/moe.h)."""
+    if grad_logits is None:
+        grad_logits = torch.empty((desc.num_tokens, desc.num_experts), dtype=desc.logits_dtype, device=logits.device)
+    prepare_route_backward(desc, logits, topk_idx, grad_weights, grad_logits, stream)()
+    return grad_logits
+
+
+def swiglu_checkpoint(desc: MoeGluDesc, device):
+    """Fresh checkpoint buffers: (codes uint8 [rows, 2F], scales fp32 [rows, 2 * ceil(F/128)])."""
+    return (torch.empty((desc.rows, 2 * desc.width), dtype=torch.uint8, device=device),
+            torch.empty((desc.rows, 2 * desc.groups), dtype=torch.float32, device=device))
+
+
+def _want_checkpoint(desc: MoeGluDesc, ckpt, ckpt_scales, optional: bool):
+    _want("ckpt", ckpt, torch.uint8, desc.rows * 2 * desc.width, optional)
+    _want("ckpt_scales", ckpt_scales, torch.float32, desc.rows * 2 * desc.groups, optional)
+
+
+def prepare_swiglu(desc: MoeGluDesc, gate_up, act, ckpt=None, ckpt_scales=None, num_rows=None, stream=None) -> Prepared:
+    _want("num_rows", num_rows, torch.int32, 1, optional=True)
+    _want("gate_up", gate_up, torch.bfloat16, desc.rows * 2 * desc.width)
+    _want("act", act, torch.bfloat16, desc.rows * desc.width, optional=True)
+    _want_checkpoint(desc, ckpt, ckpt_scales, optional=True)
+    d = desc.c()
+    args = (ctypes.byref(d), *_vps(num_rows, gate_up, act, ckpt, ckpt_scales), ctypes.c_void_p(_stream(stream)))
+    return Prepared("moe_swiglu", args, (d, num_rows, gate_up, act, ckpt, ckpt_scales))
+
+
+def moe_swiglu(desc: MoeGluDesc, gate_up, act=None, ckpt=None, ckpt_scales=None, num_rows=None, stream=None):
+    """act = silu(gate) * up, and the checkpoint if buffers for it are given. Returns act bf16 [rows, F]."""
+    if act is None:
+        act = torch.empty((desc.rows, desc.width), dtype=torch.bfloat16, device=gate_up.device)
+    prepare_swiglu(desc, gate_up, act, ckpt, ckpt_scales, num_rows, stream)()
+    return act
+
+
+def prepare_swiglu_backward(desc: MoeGluDesc, ckpt, ckpt_scales, grad_act, grad_gate_up, act=None, num_rows=None,
+                            stream=None) -> Prepared:
+    _want("num_rows", num_rows, torch.int32, 1, optional=True)
+    _want_checkpoint(desc, ckpt, ckpt_scales, optional=False)
+    _want("grad_act", grad_act, torch.bfloat16, desc.rows * desc.width)
+    _want("grad_gate_up", grad_gate_up, torch.bfloat16, desc.rows * 2 * desc.width)
+    _want("act", act, torch.bfloat16, desc.rows * desc.width, optional=True)
+    d = desc.c()
+    args = (ctypes.byref(d), *_vps(num_rows, ckpt, ckpt_scales, grad_act, grad_gate_up, act),
+            ctypes.c_void_p(_stream(stream)))
+    return Prepared("moe_swiglu_backward", args, (d, num_rows, ckpt, ckpt_scales, grad_act, grad_gate_up, act))
+
+
+def moe_swiglu_backward(desc: MoeGluDesc, ckpt, ckpt_scales, grad_act, grad_gate_up=None, act=None, num_rows=None,
+                        stream=None):
+    """Gradient of gate|up from the checkpoint; act (if given) receives the activation again.
+    Returns grad_gate_up bf16 [rows, 2F]."""
+    if grad_gate_up is None:
+        grad_gate_up = torch.empty((desc.rows, 2 * desc.width), dtype=torch.bfloat16, device=grad_act.device)
+    prepare_swiglu_backward(desc, ckpt, ckpt_scales, grad_act, grad_gate_up, act, num_rows, stream)()
+    return grad_gate_up
+
+
+def expert_row_ranges(lay: dict):
+    """(row_begin, row_end) of rows in slot order, from moe_layout's outputs (views, no copy)."""
+    off = lay["expert_offset"]
+    return off[:-1], off[1:]
+
+
+def _want_experts(desc: MoeExpertDesc, row_begin, row_end):
+    _want("row_begin", row_begin, torch.int32, desc.num_experts)
+    _want("row_end", row_end, torch.int32, desc.num_experts)
+
+
+def prepare_expert_product(desc: MoeExpertDesc, x, row_begin, row_end, w, y, stream=None) -> Prepared:
+    e, r, k, n = desc.num_experts, desc.rows, desc.in_features, desc.out_features
+    _want_experts(desc, row_begin, row_end)
+    _want_rows("x", x, r, k, desc.x_stride or k)
+    _want("w", w, torch.bfloat16, e * n * k)
+    _want("y", y, torch.bfloat16, r * n)
+    d = desc.c()
+    args = (ctypes.byref(d), *_vps(x, row_begin, row_end, w, y), ctypes.c_void_p(_stream(stream)))
+    return Prepared("moe_expert_product", args, (d, x, row_begin, row_end, w, y))
+
+
+def moe_expert_product(desc: MoeExpertDesc, x, row_begin, row_end, w, y=None, stream=None):
+    """y[s] = w[e] x[s] for the rows of every expert (see include/moe.h). Returns y bf16 [rows, N]."""
+    if y is None:
+        y = torch.empty((desc.rows, desc.out_features), dtype=torch.bfloat16, device=w.device)
+    prepare_expert_product(desc, x, row_begin, row_end, w, y, stream)()
+    return y
+
+
+def prepare_expert_swiglu(desc: MoeExpertDesc, x, row_begin, row_end, w, act, ckpt=None, ckpt_scales=None,
+                          stream=None) -> Prepared:
+    e, r, k, f = desc.num_experts, desc.rows, desc.in_features, desc.out_features
+    _want_experts(desc, row_begin, row_end)
+    _want_rows("x", x, r, k, desc.x_stride or k)
+    _want("w", w, torch.bfloat16, e * 2 * f * k)
+    _want("act", act, torch.bfloat16, r * f)
+    _want_checkpoint(MoeGluDesc(r, f), ckpt, ckpt_scales, optional=True)
+    d = desc.c()
+    args = (ctypes.byref(d), *_vps(x, row_begin, row_end, w, act, ckpt, ckpt_scales), ctypes.c_void_p(_stream(stream)))
+    return Prepared("moe_expert_swiglu", args, (d, x, row_begin, row_end, w, act, ckpt, ckpt_scales))
+
+
+def moe_expert_swiglu(desc: MoeExpertDesc, x, row_begin, row_end, w, act=None, ckpt=None, ckpt_scales=None, stream=None):
+    """silu(gate) * up with gate|up = w[e] x[s], w [E, 2F, K], desc.out_features = F; and the checkpoint if buffers
+    for it are given (swiglu_checkpoint). Returns act bf16 [rows, F]."""
+    if act is None:
+        act = torch.empty((desc.rows, desc.out_features), dtype=torch.bfloat16, device=w.device)
+    prepare_expert_swiglu(desc, x, row_begin, row_end, w, act, ckpt, ckpt_scales, stream)()
+    return act
+
+
+def prepare_expert_product_backward_input(desc: MoeExpertDesc, grad_y, row_begin, row_end, w, grad_x,
+                                          stream=None) -> Prepared:
+    e, r, k, n = desc.num_experts, desc.rows, desc.in_features, desc.out_features
+    _want_experts(desc, row_begin, row_end)
+    _want("grad_y", grad_y, torch.bfloat16, r * n)
+    _want("w", w, torch.bfloat16, e * n * k)
+    _want("grad_x", grad_x, torch.bfloat16, r * k)
+    d = desc.c()
+    args = (ctypes.byref(d), *_vps(grad_y, row_begin, row_end, w, grad_x), ctypes.c_void_p(_stream(stream)))
+    return Prepared("moe_expert_product_backward_input", args, (d, grad_y, row_begin, row_end, w, grad_x))
+
+
+def moe_expert_product_backward_input(desc: MoeExpertDesc, grad_y, row_begin, row_end, w, grad_x=None, stream=None):
+    """grad_x[s] = w[e]^T grad_y[s]. Returns grad_x bf16 [rows, K]."""
+    if grad_x is None:
+        grad_x = torch.empty((desc.rows, desc.in_features), dtype=torch.bfloat16, device=w.device)
+    prepare_expert_product_backward_input(desc, grad_y, row_begin, row_end, w, grad_x, stream)()
+    return grad_x
+
+
+def prepare_expert_product_backward_weight(desc: MoeExpertDesc, grad_y, x, row_begin, row_end, grad_w,
+                                           grad_kind: int = MOE_GRAD_BF16, stream=None) -> Prepared:
+    e, r, k, n = desc.num_experts, desc.rows, desc.in_features, desc.out_features
+    _want_experts(desc, row_begin, row_end)
+    _want("grad_y", grad_y, torch.bfloat16, r * n)
+    _want_rows("x", x, r, k, desc.x_stride or k)
+    _want("grad_w", grad_w, torch.bfloat16 if grad_kind == MOE_GRAD_BF16 else torch.float32, e * n * k)
+    d = desc.c()
+    args = (ctypes.byref(d), *_vps(grad_y, x, row_begin, row_end, grad_w), ctypes.c_int(grad_kind),
+            ctypes.c_void_p(_stream(stream)))
+    return Prepared("moe_expert_product_backward_weight", args, (d, grad_y, x, row_begin, row_end, grad_w))
+
+
+def moe_expert_product_backward_weight(desc: MoeExpertDesc, grad_y, x, row_begin, row_end, grad_w=None,
+                                       grad_kind: int = MOE_GRAD_BF16, stream=None):
+    """grad_w[e] = sum of grad_y[s]^T x[s] over e's rows, written as bf16 or fp32 or added to an fp32 grad_w.
+    Returns grad_w [E, N, K]."""
+    if grad_w is None:
+        grad_w = torch.zeros((desc.num_experts, desc.out_features, desc.in_features), device=row_begin.device,
+                             dtype=torch.bfloat16 if grad_kind == MOE_GRAD_BF16 else torch.float32)
+    prepare_expert_product_backward_weight(desc, grad_y, x, row_begin, row_end, grad_w, grad_kind, stream)()
+    return grad_w
+
+
 def exported_symbols() -> list[str]:
     return ["moe_strerror", "moe_record_layout", "moe_workspace_size", "moe_layout",
             "moe_layout_status", "moe_dispatch", "moe_combine", "moe_pack_record",
@@ -787,4 +1112,6 @@ def exported_symbols() -> list[str]:
             "moe_dispatch_ranks", "moe_combine_gather_ranks", "moe_ll_layout",
             "moe_dispatch_ll", "moe_combine_backward", "moe_dispatch_backward",
             "moe_combine_gather_ranks_backward", "moe_layout_dispatch", "moe_device_status",
-            "moe_layout_ranks", "moe_layout_ll", "moe_layout_ll_dispatch", "moe_set_wait_limit_ns"]
+            "moe_layout_ranks", "moe_layout_ll", "moe_layout_ll_dispatch", "moe_set_wait_limit_ns",
+            "moe_route", "moe_route_backward", "moe_swiglu", "moe_swiglu_backward", "moe_expert_product",
+            "moe_expert_swiglu", "moe_expert_product_backward_input", "moe_expert_product_backward_weight"]

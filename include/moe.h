@@ -28,7 +28,9 @@
  * per-(token, rank) layout, dispatch and gathered combine of DeepEP's normal
  * kernels; the fixed-capacity, expert-major buffers of its low-latency
  * kernels; the backward of combine and dispatch; the decode all-gather's
- * rank-slot packing and padded-token mask; an allocation-free layout.
+ * rank-slot packing and padded-token mask; an allocation-free layout; the
+ * router, the experts' products and the gated activation with its 8-bit
+ * checkpoint, which complete an MoE layer around dispatch and combine.
  *
  * Conventions
  *  - Every function returns an int status: MOE_OK (0) or a negative MOE_ERR_*
@@ -557,6 +559,166 @@ int moe_pack_record(const moe_desc_t* desc, int32_t src_token, int32_t slot_j, i
 int moe_unpack_record(const moe_desc_t* desc, const void* record, int32_t* src_token,
                       int32_t* slot_j, int32_t* expert, int32_t* ids_row, float* w_row,
                       void* payload_row, void* scales_row);
+
+/* ---- router ---------------------------------------------------------------
+ * From a router's logits to the ids and weights that the calls above take.
+ * The reference's pages start at topk_idx and topk_weights; the routing rules
+ * are those of the two families its workloads name: softmax or sigmoid
+ * scores, a balance bias that orders experts but is not part of the weights,
+ * and group-limited selection (DeepEP README, performance table setting:
+ * top-4 groups, then top-8 experts). */
+#define MOE_SCORE_SOFTMAX 0
+#define MOE_SCORE_SIGMOID 1
+#define MOE_GROUP_MAX 0      /* a group counts as its largest key */
+#define MOE_GROUP_TOP2_SUM 1 /* a group counts as the sum of its two largest keys */
+#define MOE_LOGITS_F32 0
+#define MOE_LOGITS_BF16 1
+#define MOE_MAX_GROUPS 32
+
+/* num_tokens N >= 0; num_experts E in [1, 1024]; topk k in [1, 32];
+ * num_groups G in [1, 32] with E % G == 0 (1: no groups); topk_groups in
+ * [1, G] with k <= topk_groups * E / G. logits_stride: elements between the
+ * rows of logits, >= E (0: E). scale: finite. */
+typedef struct {
+  int32_t num_tokens;
+  int32_t num_experts;
+  int32_t topk;
+  int32_t num_groups;
+  int32_t topk_groups;
+  int32_t score;        /* MOE_SCORE_* */
+  int32_t group_score;  /* MOE_GROUP_*, used when num_groups > 1 */
+  int32_t renormalize;  /* divide the weights by their sum */
+  int32_t logits_kind;  /* MOE_LOGITS_* */
+  int32_t logits_stride;
+  float scale;
+} moe_route_desc_t;
+
+/* Chooses k experts for each token.
+ *   x       the token's logits; -inf or NaN takes an expert out for the token,
+ *           +inf counts as the largest finite value
+ *   s       softmax(x) over the experts not taken out, or sigmoid(x)
+ *   key     s + bias, compared as in 64-bit arithmetic; without a bias the
+ *           experts are ordered by x itself, which orders as s does. A bias of
+ *           -inf or NaN takes an expert out of the choice (not of the softmax).
+ *   groups  (G > 1) group g holds experts [g*E/G, (g+1)*E/G) and counts as its
+ *           largest key or the sum of its two largest (of s where there is no
+ *           bias; a missing second counts as 0); the topk_groups groups with
+ *           the largest counts stay. Ties go to the lower index.
+ *   ids     the k experts with the largest keys in those groups, in descending
+ *           order, ties to the lower index
+ *   weights scale * s, or scale * s / (sum of s over the chosen) with
+ *           renormalize
+ * Where fewer than k experts are left, the remaining ids are -1 (which every
+ * call above takes as "no expert") and their weights 0; a token without any
+ * gets a row of -1. Scores, sums and weights are fp32; where the fp32 keys
+ * cannot tell the order for certain, it is settled in fp64.
+ * Inputs (device): logits fp32 or bf16 [N, E]; bias fp32 [E] or NULL.
+ * Outputs (device): topk_idx int32 [N, k]; topk_weights fp32 [N, k].
+ * Pointers aligned to their element; 16-byte aligned rows are read faster.
+ * Errors: INVALID_ARG, SHAPE, ALIGNMENT, CUDA. */
+int moe_route(const moe_route_desc_t* desc, const void* logits, const float* bias, int32_t* topk_idx,
+              float* topk_weights, moe_stream_t stream);
+
+/* Gradient of the logits from that of the weights (the choice itself has no
+ * gradient, and the bias takes no part in the weights). With G the incoming
+ * gradients of the chosen, w their weights:
+ *   sigmoid              scale * G * s * (1 - s)
+ *   sigmoid, renormalize w * (1 - s) * (G - sum(G * w) / scale)
+ *   softmax              s * (scale * G - sum(scale * G * s)), G = 0 for the rest
+ *   softmax, renormalize w * (G - sum(G * w) / scale)
+ * and 0 for experts that are not chosen, but for softmax without renormalize.
+ * topk_idx is the forward's; -1 ids are skipped, as are ids outside [0, E).
+ * A row's ids are distinct. grad_weights fp32 [N, k]; grad_logits
+ * [N, E] dense, of the logits' kind, fully written. fp32 throughout, one
+ * rounding to bf16 at the end. Errors: INVALID_ARG, SHAPE, ALIGNMENT, CUDA. */
+int moe_route_backward(const moe_route_desc_t* desc, const void* logits, const int32_t* topk_idx,
+                       const float* grad_weights, void* grad_logits, moe_stream_t stream);
+
+/* ---- gated activation with an 8-bit checkpoint ----------------------------
+ * act = silu(gate) * up, and for training the checkpoint from which the
+ * backward pass works instead of the bf16 gate and up: e4m3 codes with one
+ * fp32 scale per 128 channels of each half (the rule of
+ * MOE_PAYLOAD_FP8_E4M3_B128), 2F + 8 * ceil(F/128) bytes a row instead of 4F
+ * (and of 2F more for act, which the backward computes again). */
+typedef struct {
+  int64_t rows;  /* rows of the buffers, in [0, 2^31) */
+  int32_t width; /* F, channels of act: a multiple of 8 in [8, 65536] */
+} moe_glu_desc_t;
+
+/* gate_up bf16 [rows, 2F] (gate, then up) -> act bf16 [rows, F]; with ckpt
+ * uint8 [rows, 2F] (codes of gate, then up) and ckpt_scales fp32
+ * [rows, 2 * ceil(F/128)] (gate's groups, then up's; both NULL: none). act may
+ * be NULL where only the checkpoint is wanted. num_rows (device int32, may be
+ * NULL) limits the work to rows below *num_rows, e.g. &expert_offset[E]; the
+ * other rows are not touched. Arithmetic is fp32 with one rounding. bf16
+ * buffers 16-byte aligned, ckpt 8-byte. Errors: INVALID_ARG, SHAPE, ALIGNMENT,
+ * CUDA. */
+int moe_swiglu(const moe_glu_desc_t* desc, const int32_t* num_rows, const void* gate_up, void* act, void* ckpt,
+               float* ckpt_scales, moe_stream_t stream);
+
+/* From the checkpoint g, u (code * scale) and grad_act bf16 [rows, F], with
+ * sig = 1 / (1 + exp(-g)):
+ *   grad_gate_up[:, :F] = grad_act * u * sig * (1 + g * (1 - sig))
+ *   grad_gate_up[:, F:] = grad_act * g * sig
+ *   act                 = g * sig * u          (may be NULL)
+ * bf16 [rows, 2F] and [rows, F]; act is what the second product's weight
+ * gradient needs again. num_rows as above. Errors: INVALID_ARG, SHAPE,
+ * ALIGNMENT, CUDA. */
+int moe_swiglu_backward(const moe_glu_desc_t* desc, const int32_t* num_rows, const void* ckpt,
+                        const float* ckpt_scales, const void* grad_act, void* grad_gate_up, void* act,
+                        moe_stream_t stream);
+
+/* ---- the experts' products ------------------------------------------------
+ * Each expert's weight matrix applied to the expert's rows. Expert e owns the
+ * rows [row_begin[e], row_end[e]) of the row buffers (device int32 [E] each,
+ * clipped to [0, rows)): expert_offset and expert_offset + 1 for rows in slot
+ * order, or e * capacity and that plus recv_count[e] for the fixed-capacity
+ * buffers. The counts are read on the device, so a captured graph stays valid
+ * as the routing changes. Ranges are disjoint; rows in no range are not
+ * touched. x may be strided, so that rows can be read where dispatch put them
+ * (records + off_payload with x_stride = record_bytes / 2 for BF16 records). */
+typedef struct {
+  int64_t rows;         /* rows of the row buffers, in [0, 2^31 - 128) */
+  int64_t x_stride;     /* elements between rows of x, >= in_features, % 8 == 0 (0: in_features) */
+  int32_t num_experts;  /* E in [1, 1024] */
+  int32_t in_features;  /* K, % 8 == 0, in [8, 65536] */
+  int32_t out_features; /* N, % 8 == 0, in [8, 65536]; of moe_expert_swiglu: F, the width of act */
+} moe_expert_desc_t;
+
+/* y[s, n] = bf16_rn( sum_k x[s, k] * w[e, n, k] ), s in expert e's rows.
+ * x bf16 [rows, K] (x_stride), w bf16 [E, N, K], y bf16 [rows, N]; products of
+ * bf16 are accumulated in fp32. Buffers 16-byte aligned. The waits inside are
+ * bounded as moe_device_status describes. Errors: INVALID_ARG, SHAPE,
+ * ALIGNMENT, CUDA. */
+int moe_expert_product(const moe_expert_desc_t* desc, const void* x, const int32_t* row_begin,
+                       const int32_t* row_end, const void* w, void* y, moe_stream_t stream);
+
+/* The first product with the activation in its epilogue: w bf16 [E, 2F, K]
+ * (gate rows, then up rows), act bf16 [rows, F] = silu(gate) * up from the
+ * fp32 accumulators, and the checkpoint of the same fp32 values in the format
+ * of moe_swiglu (both NULL: none). gate and up never reach memory in bf16.
+ * Errors: as moe_expert_product. */
+int moe_expert_swiglu(const moe_expert_desc_t* desc, const void* x, const int32_t* row_begin,
+                      const int32_t* row_end, const void* w, void* act, void* ckpt, float* ckpt_scales,
+                      moe_stream_t stream);
+
+/* grad_x[s, k] = bf16_rn( sum_n grad_y[s, n] * w[e, n, k] ): grad_y bf16
+ * [rows, N], grad_x bf16 [rows, K], both dense (x_stride is not used).
+ * Errors: as moe_expert_product. */
+int moe_expert_product_backward_input(const moe_expert_desc_t* desc, const void* grad_y,
+                                      const int32_t* row_begin, const int32_t* row_end, const void* w,
+                                      void* grad_x, moe_stream_t stream);
+
+/* grad_w[e, n, k] = sum over expert e's rows s of grad_y[s, n] * x[s, k], in
+ * [E, N, K]: bf16, fp32, or added to what an fp32 buffer holds (gradients of
+ * several micro-batches). An expert without rows gets zeros (nothing with
+ * MOE_GRAD_F32_ADD). Errors: as moe_expert_product. */
+#define MOE_GRAD_BF16 0
+#define MOE_GRAD_F32 1
+#define MOE_GRAD_F32_ADD 2
+int moe_expert_product_backward_weight(const moe_expert_desc_t* desc, const void* grad_y, const void* x,
+                                       const int32_t* row_begin, const int32_t* row_end, void* grad_w,
+                                       int grad_kind, moe_stream_t stream);
 
 #ifdef __cplusplus
 }

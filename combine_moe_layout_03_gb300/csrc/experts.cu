@@ -6,17 +6,30 @@
 //   grad input    dx[s, k] = sum_n dy[s, n] w[e, n, k]
 //   grad weight   dw[e, n, k] = sum_s dy[s, n] x[s, k]
 //
-// One persistent block per SM walks over the 128 x 256 output tiles of all
-// experts, which it finds from the row ranges on the device. Warp 0 brings
-// operand tiles of 64 reduction steps into shared memory with TMA (128-byte
-// swizzle), warp 1 issues tcgen05.mma (bf16 in, fp32 accumulators in tensor
-// memory), warps 2-5 read finished accumulators and store them. Tensor memory
-// holds two accumulators of 256 columns, so a tile's epilogue runs while the
-// next one is multiplied. The reduction runs along the stored rows of both
-// operands in the forward product (K-major operands); the gradients read the
-// same buffers with the reduction across rows (MN-major operands), so nothing
-// is transposed in memory.
+// A pair of blocks (a cluster of two, tcgen05 cta_group::2) walks over output
+// tiles of all experts, which it finds from the row ranges on the device. The
+// tile's 256 M indices are features, 128 to a block, and its N indices up to
+// 256 rows of one expert (256 columns of dw): an expert's rows are covered in
+// steps of 32, so ragged experts cost little, and a few rows cost little more
+// than reading the weights once. Each block brings its own 128 features and
+// half of the N operand, 64 reduction steps at a time, so a block moves 32 KB
+// per 128 x 256 x 64 products through L2 and shared memory, which is what a
+// single block with a tile of that size (48 KB) is bound by.
+//
+// Warp 0 loads with TMA (128-byte swizzle) into six stages; warp 1 of the even
+// block issues tcgen05.mma (bf16 in, fp32 accumulators in tensor memory) for
+// both; warps 2-5 of each block store what is finished. Tensor memory holds
+// two accumulators of 256 columns, so a tile's epilogue runs while the next
+// one is multiplied. The forward product's operands are stored along the
+// reduction (K-major); the gradients read the same buffers across it
+// (MN-major), so nothing is transposed in memory.
+//
+// The accumulators of the row products lie feature by feature; 32 rows at a
+// time they cross shared memory and leave as one bulk copy per row. dw leaves
+// as TMA boxes, added in L2 where it accumulates.
 #include <cuda.h>
+
+#include <mutex>
 
 #include "moe_internal.cuh"
 
@@ -26,49 +39,137 @@ namespace {
 
 enum { kForward = 0, kGlu = 1, kGradInput = 2, kGradWeight = 3 };
 
-constexpr int kTileM = 128, kTileN = 256, kTileK = 64;
-constexpr int kBytesA = kTileM * kTileK * 2, kBytesB = kTileN * kTileK * 2;
-constexpr int kStages = 4;
+constexpr int kTileM = 256, kTileN = 256, kTileK = 64;  // of a pair
+constexpr int kHalfM = 128;                             // of a block
+constexpr int kBytesA = kHalfM * kTileK * 2, kBytesB = kTileN / 2 * kTileK * 2;
+constexpr int kStages = 6;
 constexpr int kExpertThreads = 192;
 constexpr int kTmemColumns = 512;
+constexpr int kChunk = 32;                   // rows that cross shared memory together
+constexpr int kChunkBytes = kChunk * 256;    // a row's part: 128 features in bf16, or 64 and their codes
+constexpr int kBoxBytes = 4096;              // 32 rows of 128 bytes of dw
 
 __device__ int32_t g_expert_status;  // MOE_OK, or MOE_ERR_TIMEOUT once a wait gave up
 
-// ---- tcgen05 and TMA --------------------------------------------------------
+// ---- clusters, tcgen05 and TMA ------------------------------------------------
 
-__device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The address of a shared variable in block `rank` of the cluster.
+__device__ __forceinline__ uint32_t in_block(const void* p, uint32_t rank) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ void arrive_at(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void arrive_expect_at(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
+               : "memory");
+}
+// mbar_wait for barriers that the other block arrives at.
+__device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity, uint64_t limit_ns = kWaitLimitNs) {
+  uint64_t t0 = 0;
+  while (true) {
+    uint32_t ok;
+    if (limit_ns < kWaitLimitNs)  // a lowered budget (test hook): poll without suspending
+      asm volatile(
+          "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+          "selp.u32 %0, 1, 0, p;\n\t}"
+          : "=r"(ok)
+          : "r"(smem_u32(bar)), "r"(parity)
+          : "memory");
+    else
+      asm volatile(
+          "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+          "selp.u32 %0, 1, 0, p;\n\t}"
+          : "=r"(ok)
+          : "r"(smem_u32(bar)), "r"(parity)
+          : "memory");
+    if (ok) return true;
+    const uint64_t now = global_timer_ns();
+    if (t0 == 0) t0 = now;
+    if (now - t0 > limit_ns) return false;
+  }
+}
+// All lanes wait, and leave together.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
+  return __all_sync(0xffffffffu, wait_cluster(bar, parity, limit_ns));
+}
+
+// The four epilogue warps: a barrier, and whether all of them came with yes (a
+// wait that gave up ends the loop in all of them, so that none waits alone).
+__device__ __forceinline__ bool epilogue_agrees(bool yes) {
+  uint32_t all;
   asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
-          smem_u32(dst)),
-      "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar))
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\tbarrier.cta.red.and.pred q, 1, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(all)
+      : "r"((uint32_t)yes)
+      : "memory");
+  return all != 0;
+}
+__device__ __forceinline__ void epilogue_sync() { asm volatile("barrier.cta.sync 1, 128;" ::: "memory"); }
+
+// Box into this block's shared memory; the bytes are counted at bar, in either
+// block of the pair.
+__device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 "
+      "[%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
+      "l"(map), "r"(x), "r"(y), "r"(bar)
       : "memory");
 }
-__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
   asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
-          smem_u32(dst)),
-      "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 "
+      "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
       : "memory");
+}
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void* src, int x, int y, int z) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map),
+               "r"(x), "r"(y), "r"(z), "r"(smem_u32(src))
+               : "memory");
+}
+__device__ __forceinline__ void tma_add_3d(const CUtensorMap* map, const void* src, int x, int y, int z) {
+  asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map),
+               "r"(x), "r"(y), "r"(z), "r"(smem_u32(src))
+               : "memory");
+}
+// At most one of this thread's groups of bulk stores still reads shared memory.
+__device__ __forceinline__ void bulk_wait_read_one() {
+  asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
 }
 __device__ __forceinline__ void tmem_alloc(uint32_t* dst, uint32_t columns) {
-  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst)), "r"(columns)
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst)), "r"(columns)
                : "memory");
-  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
 }
 __device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t columns) {
-  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(columns));
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(columns));
 }
 __device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
   asm volatile(
       "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
       "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
       : "memory");
 }
-// Arrives on bar when every MMA issued so far by this thread has completed.
+// Arrives on bar in both blocks when every MMA issued so far by this thread has completed.
 __device__ __forceinline__ void mma_commit(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
-               : "memory");
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          smem_u32(bar)),
+      "h"((uint16_t)3)
+      : "memory");
 }
 __device__ __forceinline__ void tmem_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tmem_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -103,198 +204,254 @@ __device__ __forceinline__ uint64_t operand_desc(uint32_t addr, bool mn_major) {
 }
 // Instruction descriptor: fp32 accumulators (bit 4), bf16 A and B (bits 7 and
 // 10), MN-major A and B (bits 15 and 16), N / 8 in bits 17-22, M / 16 in 24-28.
-__host__ __device__ constexpr uint32_t instr_desc(bool a_mn, bool b_mn, int n) {
+__device__ __forceinline__ uint32_t instr_desc(bool a_mn, bool b_mn, int n) {
   return 1u << 4 | 1u << 7 | 1u << 10 | (a_mn ? 1u << 15 : 0) | (b_mn ? 1u << 16 : 0) | (uint32_t)(n / 8) << 17 |
          (uint32_t)(kTileM / 16) << 24;
 }
 
 struct ExpertMaps {
-  CUtensorMap a, b;
+  CUtensorMap a;     // features: w, or dy of the weight gradient
+  CUtensorMap b[4];  // rows, in boxes of 16, 32, 64 and 128; the weight gradient's x in b[0]
+  CUtensorMap out;   // dw
 };
 
-// One output tile.
+// One output tile of a pair.
 struct Tile {
-  int e, m0, c0;  // expert, first row (a row of w for the weight gradient), first column
+  int e, f0;      // expert, first feature
+  int n0, n;      // first row of the expert (column of dw), and how many; n a multiple of 32
   int lo, rows;   // the expert's rows
 };
 
-struct ExpertSmem {
-  uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2];
+struct ExpertControl {
+  uint64_t full[kStages], empty[kStages], tail[kStages], acc_full[2], acc_empty[2], most_full;
   uint32_t tmem;
-  int32_t lo[MOE_MAX_EXPERTS], rows[MOE_MAX_EXPERTS];
-  int32_t first[MOE_MAX_EXPERTS + 1];  // row tiles before expert e
 };
-constexpr size_t kExpertSmemBytes = 1024 + (size_t)kStages * (kBytesA + kBytesB) + sizeof(ExpertSmem);
-
-__device__ __forceinline__ void pack_store(uint8_t* dst, const float* v) {
-  st_v4(dst, make_uint4(pack_bf16x2_rn(v[0], v[1]), pack_bf16x2_rn(v[2], v[3]), pack_bf16x2_rn(v[4], v[5]),
-                        pack_bf16x2_rn(v[6], v[7])));
+// Shared memory behind the stages: what leaves, the control block, and
+//   swiglu: the largest magnitudes of gate and up by row (two tiles), their
+//           448 / a; all row products: the tiles before each expert.
+constexpr size_t kStageBytes = kBytesA + kBytesB;
+constexpr size_t leaving_bytes(int mode) { return mode == kGradWeight ? 8 * kBoxBytes : 2 * kChunkBytes; }
+constexpr size_t glu_bytes(int mode) { return mode == kGlu ? (size_t)3 * 2 * kTileN * 4 : 0; }
+constexpr size_t expert_smem(int mode, int experts) {
+  return 1024 + kStages * kStageBytes + leaving_bytes(mode) + glu_bytes(mode) +
+         (mode == kGradWeight ? 0 : ((size_t)experts + 1) * 4) + sizeof(ExpertControl) + 16;
 }
-__device__ __forceinline__ uint2 codes8(const float* v, float inv) {
-  return make_uint2(cvt_e4m3x2(__fmul_rn(v[0], inv), __fmul_rn(v[1], inv)) |
-                        cvt_e4m3x2(__fmul_rn(v[2], inv), __fmul_rn(v[3], inv)) << 16,
-                    cvt_e4m3x2(__fmul_rn(v[4], inv), __fmul_rn(v[5], inv)) |
-                        cvt_e4m3x2(__fmul_rn(v[6], inv), __fmul_rn(v[7], inv)) << 16);
+
+// Row tiles of an expert: as few as hold its rows, of equal width in steps of
+// 32; the last is as wide as what is left.
+__device__ __forceinline__ int tiles_of(int rows) { return (rows + kTileN - 1) / kTileN; }
+
+// The rows of gate and up that one lane pair has of feature `lane % 16`: lanes
+// below 16 hold gate, the others up; afterwards the lower lanes have both of
+// the even rows, the upper lanes both of the odd ones.
+__device__ __forceinline__ void pair_up(const float (&v)[32], bool upper, float (&g)[16], float (&u)[16]) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const float give = upper ? v[2 * i] : v[2 * i + 1], keep = upper ? v[2 * i + 1] : v[2 * i];
+    const float got = __shfl_xor_sync(0xffffffffu, give, 16);
+    g[i] = upper ? got : keep;
+    u[i] = upper ? keep : got;
+  }
+}
+
+__device__ __forceinline__ uint4 pack_bf16x8(const float* v) {
+  return make_uint4(pack_bf16x2_rn(v[0], v[1]), pack_bf16x2_rn(v[2], v[3]), pack_bf16x2_rn(v[4], v[5]),
+                    pack_bf16x2_rn(v[6], v[7]));
 }
 
 template <int MODE>
 __global__ void __launch_bounds__(kExpertThreads, 1)
     k_expert(ExpertParams p, const __grid_constant__ ExpertMaps maps, uint64_t wait_ns) {
-  extern __shared__ uint8_t expert_smem[];
-  uint8_t* tiles = reinterpret_cast<uint8_t*>(((uintptr_t)expert_smem + 1023) & ~(uintptr_t)1023);
-  ExpertSmem& sm = *reinterpret_cast<ExpertSmem*>(tiles + (size_t)kStages * (kBytesA + kBytesB));
+  extern __shared__ uint8_t expert_raw[];
+  uint8_t* stages = reinterpret_cast<uint8_t*>(((uintptr_t)expert_raw + 1023) & ~(uintptr_t)1023);
+  uint8_t* leaving = stages + kStages * kStageBytes;
+  float* glu_mem = reinterpret_cast<float*>(leaving + leaving_bytes(MODE));
+  ExpertControl& sm = *reinterpret_cast<ExpertControl*>(leaving + leaving_bytes(MODE) + glu_bytes(MODE));
+  int32_t* first = reinterpret_cast<int32_t*>(&sm + 1);  // row tiles before expert e
   const int warp = threadIdx.x >> 5, lane = (int)lane_id();
   const int E = p.num_experts, K = p.in_features, N = p.out_features;
+  const uint32_t rank = cluster_rank();
+  const int64_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(&sm.full[i], 1);
+      mbar_init(&sm.full[i], 2);   // at the even block: both producers (and their bytes)
       mbar_init(&sm.empty[i], 1);
+      mbar_init(&sm.tail[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.acc_full[i], 1);
-      mbar_init(&sm.acc_empty[i], 4);
+      mbar_init(&sm.acc_empty[i], 8);  // at the even block: both blocks' epilogue warps
     }
+    mbar_init(&sm.most_full, 8);
     mbar_init_fence();
   }
   if (warp == 1) tmem_alloc(&sm.tmem, kTmemColumns);
+  if (MODE == kGlu)
+    for (int i = threadIdx.x; i < 2 * 2 * kTileN; i += kExpertThreads) glu_mem[i] = 0.0f;
   pdl_wait();
   pdl_trigger();
-  for (int e = threadIdx.x; e < E; e += kExpertThreads) {
-    const int lo = max(p.row_begin[e], 0);
-    const int hi = (int)min((int64_t)p.row_end[e], p.rows);
-    sm.lo[e] = lo;
-    sm.rows[e] = max(hi - lo, 0);
-  }
-  tmem_fence_before();
-  __syncthreads();
-  tmem_fence_after();
-  if (warp == 0) {  // row tiles before each expert
+  auto rows_of = [&](int e, int& lo) {
+    lo = max(p.row_begin[e], 0);
+    return max((int)min((int64_t)p.row_end[e], p.rows) - lo, 0);
+  };
+  if (MODE != kGradWeight && warp == 0) {
     int carry = 0;
     for (int e0 = 0; e0 < E; e0 += 32) {
       const int e = e0 + lane;
-      const int n = e < E ? (sm.rows[e] + kTileM - 1) / kTileM : 0;
+      int lo;
+      const int n = e < E ? tiles_of(rows_of(e, lo)) : 0;
       const int inc = warp_inclusive_scan(n);
-      if (e < E) sm.first[e] = carry + inc - n;
+      if (e < E) first[e] = carry + inc - n;
       carry += __shfl_sync(0xffffffffu, inc, 31);
     }
-    if (lane == 0) sm.first[E] = carry;
+    if (lane == 0) first[E] = carry;
   }
+  tmem_fence_before();
   __syncthreads();
+  cluster_sync();
+  tmem_fence_after();
   const uint32_t tmem = sm.tmem;
 
-  // Tiles in order: expert, then column tile, then row tile; blocks take
-  // every gridDim.x-th.
-  const int cols = MODE == kGradInput || MODE == kGradWeight ? K : N;
-  const int tile_cols = MODE == kGlu ? kTileN / 2 : kTileN;
-  const int across = (cols + tile_cols - 1) / tile_cols;
-  const int down = (N + kTileM - 1) / kTileM;  // weight gradient: row tiles of dw
-  const int64_t num_tiles = MODE == kGradWeight ? (int64_t)E * across * down : (int64_t)sm.first[E] * across;
+  // Tiles in order: expert, then features, then rows (columns of dw); pairs
+  // take every pairs-th, so that those running at one time share operands.
+  const int features = MODE == kGradInput ? K : N;
+  const int tile_features = MODE == kGlu ? kTileM / 2 : kTileM;
+  const int across = (features + tile_features - 1) / tile_features;
+  const int down = (K + kTileN - 1) / kTileN;  // weight gradient: column tiles
+  const int64_t num_tiles = MODE == kGradWeight ? (int64_t)E * across * down : (int64_t)first[E] * across;
   auto find = [&](int64_t t, int& e) {  // e: the expert of this warp's last tile
     Tile o;
-    int m, c;
     if (MODE == kGradWeight) {
       e = (int)(t / (across * down));
       const int i = (int)(t % (across * down));
-      m = i / across;
-      c = i % across;
+      o.f0 = i / down * tile_features;
+      o.n0 = i % down * kTileN;
+      o.n = kTileN;
+      o.rows = rows_of(e, o.lo);
     } else {
-      while (t >= (int64_t)sm.first[e + 1] * across) ++e;
-      const int n = sm.first[e + 1] - sm.first[e];
-      const int i = (int)(t - (int64_t)sm.first[e] * across);
-      m = i % n;
-      c = i / n;
+      while (t >= (int64_t)first[e + 1] * across) ++e;
+      const int many = first[e + 1] - first[e];
+      const int i = (int)(t - (int64_t)first[e] * across);
+      o.f0 = i / many * tile_features;
+      o.rows = rows_of(e, o.lo);
+      const int width = ((o.rows + many - 1) / many + 31) / 32 * 32;
+      o.n0 = i % many * width;
+      o.n = min(width, (max(o.rows - o.n0, 0) + 31) / 32 * 32);
     }
     o.e = e;
-    o.m0 = m * kTileM;
-    o.c0 = c * tile_cols;
-    o.lo = sm.lo[e];
-    o.rows = sm.rows[e];
     return o;
   };
   auto steps_of = [&](const Tile& t) {
     const int red = MODE == kGradWeight ? t.rows : MODE == kGradInput ? N : K;
-    return (red + kTileK - 1) / kTileK;
+    return t.n > 0 ? (red + kTileK - 1) / kTileK : 0;
   };
   bool ok = true;
 
-  if (warp == 0) {  // operand tiles into shared memory
+  if (warp == 0) {  // this block's operands into shared memory
     if (lane == 0) {
       int e = 0;
       int64_t issued = 0;
-      for (int64_t t = blockIdx.x; ok && t < num_tiles; t += gridDim.x) {
+      for (int64_t t = pair; ok && t < num_tiles; t += pairs) {
         const Tile o = find(t, e);
         const int steps = steps_of(o);
+        const int half = o.n / 2;
         for (int k = 0; k < steps; ++k, ++issued) {
           const int st = (int)(issued % kStages);
-          if (issued >= kStages && !mbar_wait(&sm.empty[st], (uint32_t)((issued / kStages + 1) & 1), wait_ns)) {
+          if (issued >= kStages && !wait_cluster(&sm.empty[st], (uint32_t)((issued / kStages + 1) & 1), wait_ns)) {
             ok = false;
             break;
           }
-          uint8_t* a = tiles + (size_t)st * (kBytesA + kBytesB);
+          uint8_t* a = stages + st * kStageBytes;
           uint8_t* b = a + kBytesA;
-          uint64_t* bar = &sm.full[st];
-          mbar_arrive_expect_tx(bar, kBytesA + kBytesB);
           const int k0 = k * kTileK;
           if (MODE == kGradWeight) {
-            for (int i = 0; i < kTileM / 64; ++i) tma_load_2d(a + i * 8192, &maps.a, o.m0 + i * 64, o.lo + k0, bar);
-            for (int i = 0; i < kTileN / 64; ++i) tma_load_2d(b + i * 8192, &maps.b, o.c0 + i * 64, o.lo + k0, bar);
-          } else {
-            tma_load_2d(a, &maps.a, k0, o.lo + o.m0, bar);
-            if (MODE == kForward) {
-              tma_load_3d(b, &maps.b, k0, o.c0, o.e, bar);
-            } else if (MODE == kGlu) {
-              tma_load_3d(b, &maps.b, k0, o.c0, o.e, bar);
-              tma_load_3d(b + kBytesB / 2, &maps.b, k0, N + o.c0, o.e, bar);
-            } else {
-              for (int i = 0; i < kTileN / 64; ++i) tma_load_3d(b + i * 8192, &maps.b, o.c0 + i * 64, k0, o.e, bar);
+            // a last step with rows of others goes through the zeroing below
+            const bool whole = o.rows - k0 >= kTileK;
+            const uint32_t bar = whole ? in_block(&sm.full[st], 0) : in_block(&sm.tail[st], rank);
+            arrive_expect_at(bar, kBytesA + kBytesB);
+            for (int i = 0; i < 2; ++i) {
+              tma_load_2d(a + i * 8192, &maps.a, o.f0 + (int)rank * kHalfM + i * 64, o.lo + k0, bar);
+              tma_load_2d(b + i * 8192, &maps.b[0], o.n0 + (int)rank * kHalfM + i * 64, o.lo + k0, bar);
             }
+            continue;
           }
+          const uint32_t bar = in_block(&sm.full[st], 0);
+          arrive_expect_at(bar, (uint32_t)(kBytesA + half * kTileK * 2));
+          if (MODE == kForward) {
+            tma_load_3d(a, &maps.a, k0, o.f0 + (int)rank * kHalfM, o.e, bar);
+          } else if (MODE == kGlu) {
+            // 16 features of gate, the same 16 of up, and so on
+            for (int i = 0; i < 4; ++i) {
+              tma_load_3d(a + i * 4096, &maps.a, k0, o.f0 + (int)rank * 64 + i * 16, o.e, bar);
+              tma_load_3d(a + i * 4096 + 2048, &maps.a, k0, N + o.f0 + (int)rank * 64 + i * 16, o.e, bar);
+            }
+          } else {
+            for (int i = 0; i < 2; ++i)
+              tma_load_3d(a + i * 8192, &maps.a, o.f0 + (int)rank * kHalfM + i * 64, k0, o.e, bar);
+          }
+          for (int i = 3, at = 0; i >= 0; --i)
+            if (half & (16 << i)) {
+              tma_load_2d(b + at * 128, &maps.b[i], k0, o.lo + o.n0 + (int)rank * half + at, bar);
+              at += 16 << i;
+            }
         }
       }
-      if (!ok) g_expert_status = MOE_ERR_TIMEOUT;
-      // no copy may land after the block has exited: the last phase of every
-      // stage in use, with the full budget
-      for (int64_t i = issued > kStages ? issued - kStages : 0; i < issued; ++i)
-        mbar_wait(&sm.full[i % kStages], (uint32_t)((i / kStages) & 1));
+      if (!ok) {
+        // no copy may land after the block has exited; those in flight are
+        // counted at the other block's barriers, so give them time instead
+        g_expert_status = MOE_ERR_TIMEOUT;
+        const uint64_t t0 = global_timer_ns();
+        while (global_timer_ns() - t0 < 2000000ull) {
+        }
+      }
     }
-  } else if (warp == 1) {  // tensor cores
-    constexpr bool a_mn = MODE == kGradWeight, b_mn = MODE == kGradInput || MODE == kGradWeight;
-    constexpr uint32_t idesc = instr_desc(a_mn, b_mn, kTileN);
+  } else if (warp == 1) {  // tensor cores, for both blocks
+    constexpr bool a_mn = MODE == kGradInput || MODE == kGradWeight, b_mn = MODE == kGradWeight;
     int e = 0;
     int64_t taken = 0;
-    int acc = 0;  // accumulators begun
-    for (int64_t t = blockIdx.x; ok && t < num_tiles; t += gridDim.x) {
+    int acc = 0;             // accumulators begun
+    uint32_t tail_bits = 0;  // parity of each stage's tail barrier
+    for (int64_t t = pair; ok && t < num_tiles; t += pairs) {
       const Tile o = find(t, e);
       const int steps = steps_of(o);
       if (steps == 0) continue;
       const int as = acc & 1;
-      if (acc >= 2 && !__all_sync(0xffffffffu, mbar_wait(&sm.acc_empty[as], (uint32_t)((acc / 2 + 1) & 1), wait_ns))) {
+      if (rank == 0 && acc >= 2 && !warp_wait(&sm.acc_empty[as], (uint32_t)((acc / 2 + 1) & 1), wait_ns)) {
         ok = false;
         break;
       }
+      if (MODE != kGradWeight && rank != 0) break;  // nothing to do in the odd block
       tmem_fence_after();
+      const uint32_t idesc = instr_desc(a_mn, b_mn, o.n);
       for (int k = 0; k < steps; ++k, ++taken) {
         const int st = (int)(taken % kStages);
-        if (!__all_sync(0xffffffffu, mbar_wait(&sm.full[st], (uint32_t)((taken / kStages) & 1), wait_ns))) {
+        uint8_t* a = stages + st * kStageBytes;
+        int parts = kTileK / 16;
+        if (MODE == kGradWeight && o.rows - k * kTileK < kTileK) {
+          // the rows after the expert's last belong to others: zeros instead,
+          // up to the next whole step of 16, by each block in its own stage
+          const int left = o.rows - k * kTileK;
+          parts = (left + 15) / 16;
+          if (!warp_wait(&sm.tail[st], (tail_bits >> st) & 1u, wait_ns)) {
+            ok = false;
+            break;
+          }
+          tail_bits ^= 1u << st;
+          const int zero = (parts * 16 - left) * 8;  // 16-byte pieces per 64 columns
+          for (int i = lane; i < zero; i += 32)
+            for (int c = 0; c < 4; ++c)
+              *reinterpret_cast<uint4*>(a + c * 8192 + left * 128 + i * 16) = make_uint4(0, 0, 0, 0);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) arrive_at(in_block(&sm.full[st], 0));
+        }
+        if (rank != 0) continue;
+        if (!warp_wait(&sm.full[st], (uint32_t)((taken / kStages) & 1), wait_ns)) {
           ok = false;
           break;
         }
         tmem_fence_after();
-        uint8_t* a = tiles + (size_t)st * (kBytesA + kBytesB);
-        int parts = kTileK / 16;
-        if (MODE == kGradWeight && k == steps - 1) {
-          // the rows after the expert's last belong to others: zeros instead,
-          // up to the next whole step of 16
-          const int left = o.rows - k * kTileK;
-          parts = (left + 15) / 16;
-          const int zero = (parts * 16 - left) * 8;  // 16-byte pieces per 64 columns
-          for (int i = lane; i < zero; i += 32)
-            for (int c = 0; c < (kTileM + kTileN) / 64; ++c)
-              *reinterpret_cast<uint4*>(a + c * 8192 + left * 128 + i * 16) = make_uint4(0, 0, 0, 0);
-          fence_proxy_async_smem();
-          __syncwarp();
-        }
         if (lane == 0) {
           const uint64_t da = operand_desc(smem_u32(a), a_mn), db = operand_desc(smem_u32(a + kBytesA), b_mn);
           for (int i = 0; i < parts; ++i)
@@ -309,114 +466,193 @@ __global__ void __launch_bounds__(kExpertThreads, 1)
     }
     if (!ok && lane == 0) g_expert_status = MOE_ERR_TIMEOUT;
     // tensor memory is freed below: wait for the last MMAs, with the full budget
-    if (taken > 0) mbar_wait(&sm.empty[(taken - 1) % kStages], (uint32_t)(((taken - 1) / kStages) & 1));
+    if (rank == 0 && taken > 0) wait_cluster(&sm.empty[(taken - 1) % kStages], (uint32_t)(((taken - 1) / kStages) & 1));
   } else {  // accumulators to memory: warp w reads tensor-memory lanes (w % 4) * 32 ..
     const int quarter = warp & 3;
     int e = 0;
-    int acc = 0;
-    for (int64_t t = blockIdx.x; ok && t < num_tiles; t += gridDim.x) {
+    int acc = 0, chunks = 0;
+    for (int64_t t = pair; ok && t < num_tiles; t += pairs) {
       const Tile o = find(t, e);
-      const int m = o.m0 + quarter * 32 + lane;
       const bool some = steps_of(o) > 0;  // without rows a weight gradient is zero
+      if (!some && MODE != kGradWeight) continue;
       const int as = acc & 1;
       if (some) {
-        if (!__all_sync(0xffffffffu, mbar_wait(&sm.acc_full[as], (uint32_t)((acc / 2) & 1), wait_ns))) {
-          ok = false;
-          break;
-        }
+        ok = epilogue_agrees(warp_wait(&sm.acc_full[as], (uint32_t)((acc / 2) & 1), wait_ns));
+        if (!ok) break;
         tmem_fence_after();
       }
       const uint32_t src = tmem + (uint32_t)(quarter * 32) * 65536u + (uint32_t)(as * kTileN);
-      const int width = min(cols - o.c0, tile_cols);  // columns of this tile, a multiple of 8
-      if (MODE == kGlu) {
-        const bool on = m < o.rows;
-        const int64_t row = (int64_t)o.lo + m;
-        const int groups = (N + 127) / 128;
-        float inv_g = 0.0f, inv_u = 0.0f;
-        if (p.ckpt) {  // first pass: the largest magnitudes of the group
-          float ag = 0.0f, au = 0.0f;
-          for (int c = 0; c < width; c += 32) {
-            float g[32], u[32];
-            tmem_load32(src + c, g);
-            tmem_load32(src + kTileN / 2 + c, u);
+      if (MODE == kGradWeight) {
+        // boxes of 32 rows x 128 bytes, each warp its own two buffers
+        uint8_t* mine = leaving + quarter * 2 * kBoxBytes;
+        const bool wide = p.grad_kind != MOE_GRAD_BF16;
+        const int step = wide ? 32 : 64;
+        const int n = o.f0 + (int)rank * kHalfM + quarter * 32;  // first row of dw
+        if (some || p.grad_kind != MOE_GRAD_F32_ADD)
+          for (int c = 0; c < kTileN && o.n0 + c < K && n < N; c += step, ++chunks) {
+            uint8_t* box = mine + (chunks & 1) * kBoxBytes;
+            if (lane == 0) bulk_wait_read_one();
+            __syncwarp();
+            uint4 q[8];
+            auto load = [&](int at, float (&v)[32]) {
+              if (some) {
+                tmem_load32(src + at, v);
+              } else {
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (c + i < width) {
-                ag = fmaxf(ag, fabsf(g[i]));
-                au = fmaxf(au, fabsf(u[i]));
+                for (int i = 0; i < 32; ++i) v[i] = 0.0f;
               }
-          }
-          ag = fmaxf(ag, 1e-4f);
-          au = fmaxf(au, 1e-4f);
-          inv_g = __fdiv_rn(448.0f, ag);
-          inv_u = __fdiv_rn(448.0f, au);
-          if (on) {
-            float* s = p.scales + row * 2 * groups + o.c0 / 128;
-            s[0] = __fdiv_rn(ag, 448.0f);
-            s[groups] = __fdiv_rn(au, 448.0f);
-          }
-        }
-        for (int c = 0; c < width; c += 32) {
-          float g[32], u[32];
-          tmem_load32(src + c, g);
-          tmem_load32(src + kTileN / 2 + c, u);
+            };
+            float v[32];
+            load(c, v);
+            if (wide) {
 #pragma unroll
-          for (int i = 0; i < 32; i += 8) {
-            if (!on || c + i >= width) continue;
-            const int64_t at = o.c0 + c + i;
-            float v[8];
+              for (int i = 0; i < 8; ++i)
+                q[i] = make_uint4(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]),
+                                  __float_as_uint(v[4 * i + 2]), __float_as_uint(v[4 * i + 3]));
+            } else {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = swiglu_of(g[i + j], u[i + j]);
-            pack_store(p.out + (row * N + at) * 2, v);
-            if (p.ckpt) {
-              *reinterpret_cast<uint2*>(p.ckpt + row * 2 * N + at) = codes8(g + i, inv_g);
-              *reinterpret_cast<uint2*>(p.ckpt + row * 2 * N + N + at) = codes8(u + i, inv_u);
+              for (int i = 0; i < 4; ++i) q[i] = pack_bf16x8(v + 8 * i);
+              load(c + 32, v);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) q[4 + i] = pack_bf16x8(v + 8 * i);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i)  // the swizzle that the box is stored with
+              *reinterpret_cast<uint4*>(box + lane * 128 + ((i ^ (lane & 7)) << 4)) = q[i];
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              if (p.grad_kind == MOE_GRAD_F32_ADD)
+                tma_add_3d(&maps.out, box, o.n0 + c, n, o.e);
+              else
+                tma_store_3d(&maps.out, box, o.n0 + c, n, o.e);
+              bulk_commit();
             }
           }
-        }
       } else {
-        const bool on = MODE == kGradWeight ? m < N : m < o.rows;
-        const int64_t row = MODE == kGradWeight ? (int64_t)o.e * N + m : (int64_t)o.lo + m;
-        for (int c = 0; c < width; c += 32) {
-          float v[32];
-          if (some) {
+        const int own = MODE == kGlu ? 64 : kHalfM;                // features of this block
+        const int f = o.f0 + (int)rank * own;
+        const int nf = min(max(features - f, 0), own);             // that exist, a multiple of 8
+        const int valid = min(o.n, o.rows - o.n0);                 // rows of the tile that the expert has
+        const bool codes16 = MODE == kGlu && p.ckpt && N % 16 == 0 && (uintptr_t)p.ckpt % 16 == 0;
+        const bool upper = lane >= 16;
+        const int here = MODE == kGlu ? quarter * 16 + (lane & 15) : quarter * 32 + lane;  // this lane's feature
+        float* most = glu_mem + (acc & 1) * 2 * kTileN;            // [2][row], as magnitudes
+        float* scale_up = glu_mem + 2 * 2 * kTileN;                // [2][row], 448 / a
+        if (MODE == kGlu && p.ckpt) {
+          // the largest magnitude of each row's 128 features of gate and up:
+          // over 16 lanes (each step halves the rows that a lane carries),
+          // then over the warps of both blocks
+          const uint32_t to[2] = {in_block(most, 0), in_block(most, 1)};
+          for (int c = 0; c < o.n; c += kChunk) {
+            float v[32];
             tmem_load32(src + c, v);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = here < nf ? fabsf(v[i]) : 0.0f;
+#pragma unroll
+            for (int o2 = 8, many = 16; o2 > 0; o2 >>= 1, many >>= 1) {
+              const bool high = lane & o2;
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                if (i >= many) break;
+                const float give = high ? v[i] : v[i + many], keep = high ? v[i + many] : v[i];
+                v[i] = fmaxf(keep, __shfl_xor_sync(0xffffffffu, give, o2));
+              }
+            }
+            // rows c + 2 * bits of lane, from 16 rows a step of lane bit 3
+            const int row = c + ((lane >> 3) & 1) * 16 + ((lane >> 2) & 1) * 8 + ((lane >> 1) & 1) * 4 + (lane & 1) * 2;
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+              for (int r = 0; r < 2; ++r)
+                asm volatile("red.relaxed.cluster.shared::cluster.max.u32 [%0], %1;" ::"r"(
+                                 to[r] + (uint32_t)((upper ? kTileN : 0) + row + i) * 4u),
+                             "r"(__float_as_uint(v[i]))
+                             : "memory");
+          }
+          __syncwarp();
+          if (lane < 2) arrive_at(in_block(&sm.most_full, (uint32_t)lane));
+          ok = epilogue_agrees(warp_wait(&sm.most_full, (uint32_t)(acc & 1), wait_ns));
+          if (!ok) break;
+          const int groups = (N + 127) / 128;
+          for (int i = quarter * 32 + lane; i < 2 * kTileN; i += 128) {
+            const int r = i % kTileN, h = i / kTileN;
+            const float a = fmaxf(most[i], 1e-4f);
+            scale_up[i] = __fdiv_rn(448.0f, a);
+            most[i] = 0.0f;  // for the tile after the next
+            if (rank == 0 && r < valid)
+              p.scales[((int64_t)o.lo + o.n0 + r) * 2 * groups + h * groups + o.f0 / 128] = __fdiv_rn(a, 448.0f);
+          }
+          epilogue_sync();
+        }
+        for (int c = 0; c < o.n; c += kChunk, ++chunks) {
+          uint8_t* buf = leaving + (chunks & 1) * kChunkBytes;
+          float v[32];
+          tmem_load32(src + c, v);
+          if (MODE == kGlu) {
+            float g[16], u[16];
+            pair_up(v, upper, g, u);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const int r = 2 * i + (upper ? 1 : 0);
+              uint8_t* to = buf + r * 256;
+              reinterpret_cast<uint16_t*>(to)[here] = (uint16_t)pack_bf16x2_rn(swiglu_of(g[i], u[i]), 0.0f);
+              if (p.ckpt) {
+                const uint32_t q =
+                    cvt_e4m3x2(__fmul_rn(g[i], scale_up[c + r]), __fmul_rn(u[i], scale_up[kTileN + c + r]));
+                to[128 + here] = (uint8_t)q;
+                to[192 + here] = (uint8_t)(q >> 8);
+              }
+            }
           } else {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = 0.0f;
+            for (int i = 0; i < 32; ++i)
+              reinterpret_cast<uint16_t*>(buf + i * 256)[here] = (uint16_t)pack_bf16x2_rn(v[i], 0.0f);
           }
-#pragma unroll
-          for (int i = 0; i < 32; i += 8) {
-            if (!on || c + i >= width) continue;
-            const int64_t at = row * cols + o.c0 + c + i;
-            if (MODE != kGradWeight || p.grad_kind == MOE_GRAD_BF16) {
-              pack_store(p.out + at * 2, v + i);
-            } else if (p.grad_kind == MOE_GRAD_F32 || some) {
-              float4* d = reinterpret_cast<float4*>(p.out + at * 4);
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                float4 r = make_float4(v[i + 4 * h], v[i + 4 * h + 1], v[i + 4 * h + 2], v[i + 4 * h + 3]);
-                if (p.grad_kind == MOE_GRAD_F32_ADD) {
-                  const float4 was = d[h];
-                  r = make_float4(was.x + r.x, was.y + r.y, was.z + r.z, was.w + r.w);
-                }
-                d[h] = r;
+          fence_proxy_async_smem();
+          // the copies out of the other buffer have been read; everybody has
+          // written this one
+          if (quarter == 0) bulk_wait_read_all();
+          epilogue_sync();
+          if (quarter == 0 && c + lane < valid && nf > 0) {
+            const int64_t row = (int64_t)o.lo + o.n0 + c + lane;
+            const uint8_t* from = buf + lane * 256;
+            bulk_store_s2g(p.out + (row * features + f) * 2, from, (uint32_t)nf * 2u);
+            if (codes16) {
+              bulk_store_s2g(p.ckpt + row * 2 * N + f, from + 128, (uint32_t)nf);
+              bulk_store_s2g(p.ckpt + row * 2 * N + N + f, from + 192, (uint32_t)nf);
+            }
+            bulk_commit();
+          }
+          if (MODE == kGlu && p.ckpt && !codes16) {
+            // rows of codes that start at 8 bytes
+            for (int i = quarter * 32 + lane; i < kChunk * 16; i += 128) {
+              const int r = i / 16, piece = i % 16;  // 8 pieces of gate, 8 of up
+              const int at = piece % 8 * 8;
+              if (c + r < valid && at < nf) {
+                const int64_t row = (int64_t)o.lo + o.n0 + c + r;
+                *reinterpret_cast<uint2*>(p.ckpt + row * 2 * N + piece / 8 * N + f + at) =
+                    *reinterpret_cast<const uint2*>(buf + r * 256 + 128 + piece * 8);
               }
             }
+            epilogue_sync();
           }
         }
       }
       if (some) {
         tmem_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.acc_empty[as]);
+        if (lane == 0) arrive_at(in_block(&sm.acc_empty[as], 0));
         ++acc;
       }
     }
     if (!ok && lane == 0) g_expert_status = MOE_ERR_TIMEOUT;
+    bulk_wait_read_all();
   }
+  __syncwarp();
   tmem_fence_before();
   __syncthreads();
+  cluster_sync();
   tmem_fence_after();
   if (warp == 1) tmem_free(tmem, kTmemColumns);
 }
@@ -440,18 +676,49 @@ EncodeTiled encode_tiled() {
   return fn;
 }
 
-// bf16 tensor [depth][rows][width] with `stride` elements between rows, read
-// in boxes of 64 x box_rows; what lies outside reads as zero.
+// Tensor [depth][rows][width] (two dimensions where depth is 0) of bf16 or
+// fp32 with `stride` elements between rows, in boxes of 128 bytes x box_rows;
+// what lies outside reads as zero and is not written.
 bool make_map(CUtensorMap* map, const void* base, int64_t width, int64_t rows, int64_t depth, int64_t stride,
-              int box_rows) {
+              int box_rows, bool f32 = false) {
   const EncodeTiled fn = encode_tiled();
   if (!fn) return false;
+  const cuuint64_t size = f32 ? 4 : 2;
   const cuuint64_t dims[3] = {(cuuint64_t)width, (cuuint64_t)rows, (cuuint64_t)depth};
-  const cuuint64_t strides[2] = {(cuuint64_t)stride * 2, (cuuint64_t)stride * 2 * (cuuint64_t)rows};
-  const cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1}, one[3] = {1, 1, 1};
-  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, depth > 0 ? 3 : 2, const_cast<void*>(base), dims, strides, box, one,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+  const cuuint64_t strides[2] = {(cuuint64_t)stride * size, (cuuint64_t)stride * size * (cuuint64_t)rows};
+  const cuuint32_t box[3] = {(cuuint32_t)(128 / size), (cuuint32_t)box_rows, 1}, one[3] = {1, 1, 1};
+  return fn(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, depth > 0 ? 3 : 2,
+            const_cast<void*>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The pairs that can be resident at once on the current device, looked up once
+// per device and kernel.
+template <int MODE>
+int resident_pairs(int dev, int sms) {
+  static std::once_flag once[64];
+  static int found[64];
+  if (dev >= 64) return 0;
+  std::call_once(once[dev], [&] {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(sms / 2 * 2));
+    cfg.blockDim = dim3(kExpertThreads);
+    cfg.dynamicSmemBytes = expert_smem(MODE, MOE_MAX_EXPERTS);
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = 2;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, (const void*)k_expert<MODE>, &cfg) != cudaSuccess) {
+      cudaGetLastError();
+      n = 0;
+    }
+    found[dev] = n;
+  });
+  return found[dev];
 }
 
 template <int MODE>
@@ -460,26 +727,34 @@ cudaError_t launch(const ExpertParams& p, cudaStream_t s) {
   if (!current_device(&dev, &sms)) return cudaErrorInvalidDevice;
   const int64_t K = p.in_features, N = p.out_features, E = p.num_experts;
   ExpertMaps maps;
-  bool ok;
-  if (MODE == kForward || MODE == kGlu)
-    ok = make_map(&maps.a, p.x, K, p.rows, 0, p.x_stride, kTileM) &&
-         make_map(&maps.b, p.w, K, MODE == kGlu ? 2 * N : N, E, K, MODE == kGlu ? kTileN / 2 : kTileN);
-  else if (MODE == kGradInput)
-    ok = make_map(&maps.a, p.x, N, p.rows, 0, N, kTileM) && make_map(&maps.b, p.w, K, N, E, K, kTileK);
-  else
-    ok = make_map(&maps.a, p.x, N, p.rows, 0, N, kTileK) && make_map(&maps.b, p.x2, K, p.rows, 0, p.x_stride, kTileK);
+  bool ok = true;
+  if (MODE == kGradWeight) {
+    const bool f32 = p.grad_kind != MOE_GRAD_BF16;
+    ok = make_map(&maps.a, p.x, N, p.rows, 0, N, kTileK) &&
+         make_map(&maps.b[0], p.x2, K, p.rows, 0, p.x_stride, kTileK) &&
+         make_map(&maps.out, p.out, K, N, E, K, 32, f32);
+  } else {
+    if (MODE == kForward) ok = make_map(&maps.a, p.w, K, N, E, K, kHalfM);
+    if (MODE == kGlu) ok = make_map(&maps.a, p.w, K, 2 * N, E, K, 16);
+    if (MODE == kGradInput) ok = make_map(&maps.a, p.w, K, N, E, K, kTileK);
+    const int64_t width = MODE == kGradInput ? N : K, stride = MODE == kGradInput ? N : p.x_stride;
+    for (int i = 0; i < 4; ++i) ok = ok && make_map(&maps.b[i], p.x, width, p.rows, 0, stride, 16 << i);
+  }
   if (!ok) return cudaErrorUnknown;
   const void* fn = (const void*)k_expert<MODE>;
-  cudaError_t err = ensure_dynamic_smem(fn, kExpertSmemBytes);
+  cudaError_t err = ensure_dynamic_smem(fn, expert_smem(MODE, MOE_MAX_EXPERTS));
   if (err != cudaSuccess) return err;
-  // the row counts are on the device: as many blocks as there can be tiles
-  const int64_t cols = MODE == kForward || MODE == kGlu ? N : K, width = MODE == kGlu ? kTileN / 2 : kTileN;
-  const int64_t row_tiles = MODE == kGradWeight ? E * ((N + kTileM - 1) / kTileM) : E + p.rows / kTileM;
-  const int64_t most = row_tiles * ((cols + width - 1) / width);
+  const int64_t pairs = resident_pairs<MODE>(dev, sms);
+  if (pairs < 1) return cudaErrorInvalidConfiguration;
+  // the row counts are on the device: as many pairs as there can be tiles
+  const int64_t features = MODE == kGradInput ? K : N, width = MODE == kGlu ? kTileM / 2 : kTileM;
+  const int64_t across = (features + width - 1) / width;
+  const int64_t most = across * (MODE == kGradWeight ? E * ((K + kTileN - 1) / kTileN) : E + p.rows / kTileN);
   ExpertParams q = p;
   uint64_t wait_ns = wait_limit_ns();
   void* args[] = {&q, &maps, &wait_ns};
-  return launch_pdl(fn, dim3((unsigned)(most < sms ? most : sms)), dim3(kExpertThreads), kExpertSmemBytes, s, args);
+  return launch_pdl(fn, dim3((unsigned)(2 * (most < pairs ? most : pairs))), dim3(kExpertThreads),
+                    expert_smem(MODE, p.num_experts), s, args, 2);
 }
 
 }  // namespace

@@ -25,8 +25,8 @@
 // (MN-major), so nothing is transposed in memory.
 //
 // The accumulators of the row products lie feature by feature; 32 rows at a
-// time they cross shared memory and leave as one bulk copy per row. dw leaves
-// as TMA boxes, added in L2 where it accumulates.
+// time they cross shared memory and leave as whole rows of 128 features. dw
+// leaves as TMA boxes, added in L2 where it accumulates.
 #include <cuda.h>
 
 #include <mutex>
@@ -61,6 +61,15 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+// One lane of a warp that runs together. The operations below that one thread
+// issues are predicated on it instead of standing behind a branch: the warp
+// then stays together and their operands in uniform registers. (Behind `if
+// (lane == 0)` two copies took 680 cycles a step, more than the products.)
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t on;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(on));
+  return on;
+}
 // The address of a shared variable in block `rank` of the cluster.
 __device__ __forceinline__ uint32_t in_block(const void* p, uint32_t rank) {
   uint32_t a;
@@ -70,11 +79,17 @@ __device__ __forceinline__ uint32_t in_block(const void* p, uint32_t rank) {
 __device__ __forceinline__ void arrive_at(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-__device__ __forceinline__ void arrive_expect_at(uint32_t bar, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
-               : "memory");
+// Announces copies; it orders nothing else, and a release here would wait for
+// all that the thread has under way, at every step.
+__device__ __forceinline__ void arrive_expect_at(uint32_t bar, uint32_t bytes, uint32_t on) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\t"
+      "@p mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;\n\t}" ::"r"(bar),
+      "r"(bytes), "r"(on)
+      : "memory");
 }
-// mbar_wait for barriers that the other block arrives at.
+// mbar_wait where what the other block wrote before it arrived is read next.
+// (Copies and MMAs need no such order, and it costs most of a microsecond.)
 __device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity, uint64_t limit_ns = kWaitLimitNs) {
   uint64_t t0 = 0;
   while (true) {
@@ -101,6 +116,9 @@ __device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity, uin
 }
 // All lanes wait, and leave together.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, limit_ns));
+}
+__device__ __forceinline__ bool warp_wait_cluster(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
   return __all_sync(0xffffffffu, wait_cluster(bar, parity, limit_ns));
 }
 
@@ -120,29 +138,43 @@ __device__ __forceinline__ void epilogue_sync() { asm volatile("barrier.cta.sync
 
 // Box into this block's shared memory; the bytes are counted at bar, in either
 // block of the pair.
-__device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+__device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, int x, int y, uint32_t bar, uint32_t on) {
   asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 "
-      "[%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
-      "l"(map), "r"(x), "r"(y), "r"(bar)
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+      "@p cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 "
+      "[%0], [%1, {%2, %3}], [%4];\n\t}" ::"r"(smem_u32(dst)),
+      "l"(map), "r"(x), "r"(y), "r"(bar), "r"(on)
       : "memory");
 }
-__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar, uint32_t on) {
   asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 "
-      "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
-      "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+      "@p cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 "
+      "[%0], [%1, {%2, %3, %4}], [%5];\n\t}" ::"r"(smem_u32(dst)),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar), "r"(on)
       : "memory");
 }
-__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void* src, int x, int y, int z) {
-  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map),
-               "r"(x), "r"(y), "r"(z), "r"(smem_u32(src))
-               : "memory");
+__device__ __forceinline__ void tma_load_5d(void* dst, const CUtensorMap* map, int x, int y, int z, int v, int w, uint32_t bar, uint32_t on) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %8, 0;\n\t"
+      "@p cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 "
+      "[%0], [%1, {%2, %3, %4, %5, %6}], [%7];\n\t}" ::"r"(smem_u32(dst)),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(v), "r"(w), "r"(bar), "r"(on)
+      : "memory");
 }
-__device__ __forceinline__ void tma_add_3d(const CUtensorMap* map, const void* src, int x, int y, int z) {
-  asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map),
-               "r"(x), "r"(y), "r"(z), "r"(smem_u32(src))
-               : "memory");
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void* src, int x, int y, int z, uint32_t on) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+      "@p cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];\n\t}" ::"l"(map),
+      "r"(x), "r"(y), "r"(z), "r"(smem_u32(src)), "r"(on)
+      : "memory");
+}
+__device__ __forceinline__ void tma_add_3d(const CUtensorMap* map, const void* src, int x, int y, int z, uint32_t on) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+      "@p cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2, %3}], [%4];\n\t}" ::"l"(map),
+      "r"(x), "r"(y), "r"(z), "r"(smem_u32(src)), "r"(on)
+      : "memory");
 }
 // At most one of this thread's groups of bulk stores still reads shared memory.
 __device__ __forceinline__ void bulk_wait_read_one() {
@@ -156,19 +188,20 @@ __device__ __forceinline__ void tmem_alloc(uint32_t* dst, uint32_t columns) {
 __device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t columns) {
   asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(columns));
 }
-__device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+__device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add, uint32_t on) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add), "r"(on)
       : "memory");
 }
 // Arrives on bar in both blocks when every MMA issued so far by this thread has completed.
-__device__ __forceinline__ void mma_commit(uint64_t* bar) {
+__device__ __forceinline__ void mma_commit(uint64_t* bar, uint32_t on) {
   asm volatile(
-      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\t"
+      "@p tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(
           smem_u32(bar)),
-      "h"((uint16_t)3)
+      "h"((uint16_t)3), "r"(on)
       : "memory");
 }
 __device__ __forceinline__ void tmem_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -227,28 +260,37 @@ struct ExpertControl {
   uint32_t tmem;
 };
 // Shared memory behind the stages: what leaves, the control block, and
-//   swiglu: the largest magnitudes of gate and up by row (two tiles), their
-//           448 / a; all row products: the tiles before each expert.
+//   swiglu: the largest magnitudes of gate and up by row, of both blocks and
+//           for two tiles, and their 448 / a (the partial ones of the four
+//           warps pass through the room of what leaves);
+//   all row products: the tiles before each expert.
 constexpr size_t kStageBytes = kBytesA + kBytesB;
 constexpr size_t leaving_bytes(int mode) { return mode == kGradWeight ? 8 * kBoxBytes : 2 * kChunkBytes; }
-constexpr size_t glu_bytes(int mode) { return mode == kGlu ? (size_t)3 * 2 * kTileN * 4 : 0; }
+constexpr size_t glu_bytes(int mode) { return mode == kGlu ? (size_t)5 * 2 * kTileN * 4 : 0; }
 constexpr size_t expert_smem(int mode, int experts) {
   return 1024 + kStages * kStageBytes + leaving_bytes(mode) + glu_bytes(mode) +
          (mode == kGradWeight ? 0 : ((size_t)experts + 1) * 4) + sizeof(ExpertControl) + 16;
+}
+
+__device__ __forceinline__ void next_stage(int& st, uint32_t& phase) {
+  if (++st == kStages) {
+    st = 0;
+    phase ^= 1u;
+  }
 }
 
 // Row tiles of an expert: as few as hold its rows, of equal width in steps of
 // 32; the last is as wide as what is left.
 __device__ __forceinline__ int tiles_of(int rows) { return (rows + kTileN - 1) / kTileN; }
 
-// The rows of gate and up that one lane pair has of feature `lane % 16`: lanes
-// below 16 hold gate, the others up; afterwards the lower lanes have both of
-// the even rows, the upper lanes both of the odd ones.
+// A feature's gate is in the lane whose bit 3 is clear, its up eight lanes on.
+// Of the 32 rows that both hold, the lower lane gets gate and up of the even
+// ones, the upper lane those of the odd ones.
 __device__ __forceinline__ void pair_up(const float (&v)[32], bool upper, float (&g)[16], float (&u)[16]) {
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
     const float give = upper ? v[2 * i] : v[2 * i + 1], keep = upper ? v[2 * i + 1] : v[2 * i];
-    const float got = __shfl_xor_sync(0xffffffffu, give, 16);
+    const float got = __shfl_xor_sync(0xffffffffu, give, 8);
     g[i] = upper ? got : keep;
     u[i] = upper ? keep : got;
   }
@@ -287,8 +329,6 @@ __global__ void __launch_bounds__(kExpertThreads, 1)
     mbar_init_fence();
   }
   if (warp == 1) tmem_alloc(&sm.tmem, kTmemColumns);
-  if (MODE == kGlu)
-    for (int i = threadIdx.x; i < 2 * 2 * kTileN; i += kExpertThreads) glu_mem[i] = 0.0f;
   pdl_wait();
   pdl_trigger();
   auto rows_of = [&](int e, int& lo) {
@@ -349,67 +389,74 @@ __global__ void __launch_bounds__(kExpertThreads, 1)
   bool ok = true;
 
   if (warp == 0) {  // this block's operands into shared memory
-    if (lane == 0) {
-      int e = 0;
-      int64_t issued = 0;
-      for (int64_t t = pair; ok && t < num_tiles; t += pairs) {
-        const Tile o = find(t, e);
-        const int steps = steps_of(o);
-        const int half = o.n / 2;
-        for (int k = 0; k < steps; ++k, ++issued) {
-          const int st = (int)(issued % kStages);
-          if (issued >= kStages && !wait_cluster(&sm.empty[st], (uint32_t)((issued / kStages + 1) & 1), wait_ns)) {
-            ok = false;
-            break;
+    const uint32_t on = elect_one();
+    const uint32_t full0 = in_block(&sm.full[0], 0), tail0 = in_block(&sm.tail[0], rank);
+    int e = 0, st = 0;
+    uint32_t phase = 1;  // a fresh barrier's phase before the first counts as complete
+    for (int64_t t = pair; ok && t < num_tiles; t += pairs) {
+      const Tile o = find(t, e);
+      const int steps = steps_of(o);
+      const int half = o.n / 2;
+      // the boxes of this block's half: 16 << i rows each, the largest first,
+      // two at most; rather than three, one that brings rows of no use
+      int sizes = half / 16;
+      if (__popc(sizes) > 2) sizes = 8;
+      const uint32_t bytes_b = (uint32_t)sizes * 16 * kTileK * 2;
+      for (int k = 0; k < steps; ++k) {
+        if (!warp_wait(&sm.empty[st], phase, wait_ns)) {
+          ok = false;
+          break;
+        }
+        uint8_t* a = stages + st * kStageBytes;
+        uint8_t* b = a + kBytesA;
+        const int k0 = k * kTileK;
+        uint32_t bar = full0 + 8u * st;
+        if (MODE == kGradWeight) {
+          // a last step with rows of others goes through the zeroing below
+          if (o.rows - k0 < kTileK) bar = tail0 + 8u * st;
+          arrive_expect_at(bar, kBytesA + kBytesB, on);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            tma_load_2d(a + i * 8192, &maps.a, o.f0 + (int)rank * kHalfM + i * 64, o.lo + k0, bar, on);
+            tma_load_2d(b + i * 8192, &maps.b[0], o.n0 + (int)rank * kHalfM + i * 64, o.lo + k0, bar, on);
           }
-          uint8_t* a = stages + st * kStageBytes;
-          uint8_t* b = a + kBytesA;
-          const int k0 = k * kTileK;
-          if (MODE == kGradWeight) {
-            // a last step with rows of others goes through the zeroing below
-            const bool whole = o.rows - k0 >= kTileK;
-            const uint32_t bar = whole ? in_block(&sm.full[st], 0) : in_block(&sm.tail[st], rank);
-            arrive_expect_at(bar, kBytesA + kBytesB);
-            for (int i = 0; i < 2; ++i) {
-              tma_load_2d(a + i * 8192, &maps.a, o.f0 + (int)rank * kHalfM + i * 64, o.lo + k0, bar);
-              tma_load_2d(b + i * 8192, &maps.b[0], o.n0 + (int)rank * kHalfM + i * 64, o.lo + k0, bar);
-            }
-            continue;
-          }
-          const uint32_t bar = in_block(&sm.full[st], 0);
-          arrive_expect_at(bar, (uint32_t)(kBytesA + half * kTileK * 2));
+        } else {
+          arrive_expect_at(bar, kBytesA + bytes_b, on);
           if (MODE == kForward) {
-            tma_load_3d(a, &maps.a, k0, o.f0 + (int)rank * kHalfM, o.e, bar);
+            tma_load_3d(a, &maps.a, k0, o.f0 + (int)rank * kHalfM, o.e, bar, on);
           } else if (MODE == kGlu) {
-            // 16 features of gate, the same 16 of up, and so on
-            for (int i = 0; i < 4; ++i) {
-              tma_load_3d(a + i * 4096, &maps.a, k0, o.f0 + (int)rank * 64 + i * 16, o.e, bar);
-              tma_load_3d(a + i * 4096 + 2048, &maps.a, k0, N + o.f0 + (int)rank * 64 + i * 16, o.e, bar);
-            }
+            // 8 features of gate, the same 8 of up, and so on
+            tma_load_5d(a, &maps.a, k0, 0, 0, o.f0 / 8 + (int)rank * 8, o.e, bar, on);
           } else {
+#pragma unroll
             for (int i = 0; i < 2; ++i)
-              tma_load_3d(a + i * 8192, &maps.a, o.f0 + (int)rank * kHalfM + i * 64, k0, o.e, bar);
+              tma_load_3d(a + i * 8192, &maps.a, o.f0 + (int)rank * kHalfM + i * 64, k0, o.e, bar, on);
           }
-          for (int i = 3, at = 0; i >= 0; --i)
-            if (half & (16 << i)) {
-              tma_load_2d(b + at * 128, &maps.b[i], k0, o.lo + o.n0 + (int)rank * half + at, bar);
+          const int row = o.lo + o.n0 + (int)rank * half;
+          int at = 0;
+#pragma unroll
+          for (int i = 3; i >= 0; --i)
+            if (sizes & (1 << i)) {
+              tma_load_2d(b + at * 128, &maps.b[i], k0, row + at, bar, on);
               at += 16 << i;
             }
         }
+        next_stage(st, phase);
       }
-      if (!ok) {
-        // no copy may land after the block has exited; those in flight are
-        // counted at the other block's barriers, so give them time instead
-        g_expert_status = MOE_ERR_TIMEOUT;
-        const uint64_t t0 = global_timer_ns();
-        while (global_timer_ns() - t0 < 2000000ull) {
-        }
+    }
+    if (!ok) {
+      // no copy may land after the block has exited; those in flight are
+      // counted at the other block's barriers, so give them time instead
+      if (on) g_expert_status = MOE_ERR_TIMEOUT;
+      const uint64_t t0 = global_timer_ns();
+      while (global_timer_ns() - t0 < 2000000ull) {
       }
     }
   } else if (warp == 1) {  // tensor cores, for both blocks
     constexpr bool a_mn = MODE == kGradInput || MODE == kGradWeight, b_mn = MODE == kGradWeight;
-    int e = 0;
-    int64_t taken = 0;
+    int e = 0, st = 0, last = -1;  // last: the stage of the last MMAs, and its phase
+    uint32_t phase = 0, last_phase = 0;
+    const uint32_t on = elect_one();
     int acc = 0;             // accumulators begun
     uint32_t tail_bits = 0;  // parity of each stage's tail barrier
     for (int64_t t = pair; ok && t < num_tiles; t += pairs) {
@@ -417,22 +464,23 @@ __global__ void __launch_bounds__(kExpertThreads, 1)
       const int steps = steps_of(o);
       if (steps == 0) continue;
       const int as = acc & 1;
-      if (rank == 0 && acc >= 2 && !warp_wait(&sm.acc_empty[as], (uint32_t)((acc / 2 + 1) & 1), wait_ns)) {
+      if (rank == 0 && acc >= 2 && !warp_wait_cluster(&sm.acc_empty[as], (uint32_t)((acc / 2 + 1) & 1), wait_ns)) {
         ok = false;
         break;
       }
       if (MODE != kGradWeight && rank != 0) break;  // nothing to do in the odd block
       tmem_fence_after();
       const uint32_t idesc = instr_desc(a_mn, b_mn, o.n);
-      for (int k = 0; k < steps; ++k, ++taken) {
-        const int st = (int)(taken % kStages);
+      for (int k = 0; k < steps; ++k, next_stage(st, phase)) {
         uint8_t* a = stages + st * kStageBytes;
         int parts = kTileK / 16;
+        bool zeroed = false;
         if (MODE == kGradWeight && o.rows - k * kTileK < kTileK) {
           // the rows after the expert's last belong to others: zeros instead,
           // up to the next whole step of 16, by each block in its own stage
           const int left = o.rows - k * kTileK;
           parts = (left + 15) / 16;
+          zeroed = true;
           if (!warp_wait(&sm.tail[st], (tail_bits >> st) & 1u, wait_ns)) {
             ok = false;
             break;
@@ -447,28 +495,32 @@ __global__ void __launch_bounds__(kExpertThreads, 1)
           if (lane == 0) arrive_at(in_block(&sm.full[st], 0));
         }
         if (rank != 0) continue;
-        if (!warp_wait(&sm.full[st], (uint32_t)((taken / kStages) & 1), wait_ns)) {
+        // a zeroed stage was written by both blocks' warps
+        if (!(MODE == kGradWeight && zeroed ? warp_wait_cluster(&sm.full[st], phase, wait_ns)
+                                            : warp_wait(&sm.full[st], phase, wait_ns))) {
           ok = false;
           break;
         }
         tmem_fence_after();
-        if (lane == 0) {
-          const uint64_t da = operand_desc(smem_u32(a), a_mn), db = operand_desc(smem_u32(a + kBytesA), b_mn);
-          for (int i = 0; i < parts; ++i)
+        const uint64_t da = operand_desc(smem_u32(a), a_mn), db = operand_desc(smem_u32(a + kBytesA), b_mn);
+#pragma unroll
+        for (int i = 0; i < kTileK / 16; ++i)
+          if (MODE != kGradWeight || i < parts)
             mma_bf16(tmem + as * kTileN, da + i * (a_mn ? 2048 : 32) / 16, db + i * (b_mn ? 2048 : 32) / 16, idesc,
-                     k > 0 || i > 0);
-          mma_commit(&sm.empty[st]);
-          if (k == steps - 1) mma_commit(&sm.acc_full[as]);
-        }
-        __syncwarp();
+                     k > 0 || i > 0, on);
+        mma_commit(&sm.empty[st], on);
+        if (k == steps - 1) mma_commit(&sm.acc_full[as], on);
+        last = st;
+        last_phase = phase;
       }
       ++acc;
     }
     if (!ok && lane == 0) g_expert_status = MOE_ERR_TIMEOUT;
     // tensor memory is freed below: wait for the last MMAs, with the full budget
-    if (rank == 0 && taken > 0) wait_cluster(&sm.empty[(taken - 1) % kStages], (uint32_t)(((taken - 1) / kStages) & 1));
+    if (last >= 0) mbar_wait(&sm.empty[last], last_phase);
   } else {  // accumulators to memory: warp w reads tensor-memory lanes (w % 4) * 32 ..
     const int quarter = warp & 3;
+    const uint32_t on = elect_one();
     int e = 0;
     int acc = 0, chunks = 0;
     for (int64_t t = pair; ok && t < num_tiles; t += pairs) {
@@ -491,7 +543,7 @@ __global__ void __launch_bounds__(kExpertThreads, 1)
         if (some || p.grad_kind != MOE_GRAD_F32_ADD)
           for (int c = 0; c < kTileN && o.n0 + c < K && n < N; c += step, ++chunks) {
             uint8_t* box = mine + (chunks & 1) * kBoxBytes;
-            if (lane == 0) bulk_wait_read_one();
+            if (on) bulk_wait_read_one();
             __syncwarp();
             uint4 q[8];
             auto load = [&](int at, float (&v)[32]) {
@@ -521,71 +573,71 @@ __global__ void __launch_bounds__(kExpertThreads, 1)
               *reinterpret_cast<uint4*>(box + lane * 128 + ((i ^ (lane & 7)) << 4)) = q[i];
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) {
-              if (p.grad_kind == MOE_GRAD_F32_ADD)
-                tma_add_3d(&maps.out, box, o.n0 + c, n, o.e);
-              else
-                tma_store_3d(&maps.out, box, o.n0 + c, n, o.e);
-              bulk_commit();
-            }
+            if (p.grad_kind == MOE_GRAD_F32_ADD)
+              tma_add_3d(&maps.out, box, o.n0 + c, n, o.e, on);
+            else
+              tma_store_3d(&maps.out, box, o.n0 + c, n, o.e, on);
+            if (on) bulk_commit();
           }
       } else {
         const int own = MODE == kGlu ? 64 : kHalfM;                // features of this block
         const int f = o.f0 + (int)rank * own;
         const int nf = min(max(features - f, 0), own);             // that exist, a multiple of 8
         const int valid = min(o.n, o.rows - o.n0);                 // rows of the tile that the expert has
-        const bool codes16 = MODE == kGlu && p.ckpt && N % 16 == 0 && (uintptr_t)p.ckpt % 16 == 0;
-        const bool upper = lane >= 16;
-        const int here = MODE == kGlu ? quarter * 16 + (lane & 15) : quarter * 32 + lane;  // this lane's feature
-        float* most = glu_mem + (acc & 1) * 2 * kTileN;            // [2][row], as magnitudes
-        float* scale_up = glu_mem + 2 * 2 * kTileN;                // [2][row], 448 / a
+        const bool upper = lane & 8;  // holds up
+        const int here = MODE == kGlu ? quarter * 16 + (lane >> 4) * 8 + (lane & 7) : quarter * 32 + lane;  // this lane's feature
+        float* scale_up = glu_mem + 4 * 2 * kTileN;                // [gate, up][row], 448 / a
         if (MODE == kGlu && p.ckpt) {
           // the largest magnitude of each row's 128 features of gate and up:
-          // over 16 lanes (each step halves the rows that a lane carries),
-          // then over the warps of both blocks
-          const uint32_t to[2] = {in_block(most, 0), in_block(most, 1)};
+          // over the 16 lanes that hold one of the two (each step halves the
+          // rows that a lane carries), over the four warps, and over the two
+          // blocks, each of which gives its own to the other
+          float* part = reinterpret_cast<float*>(leaving);         // [4 warps][gate, up][row]
+          float* most = glu_mem + (acc & 1) * 2 * 2 * kTileN;      // [block][gate, up][row]
           for (int c = 0; c < o.n; c += kChunk) {
             float v[32];
             tmem_load32(src + c, v);
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = here < nf ? fabsf(v[i]) : 0.0f;
 #pragma unroll
-            for (int o2 = 8, many = 16; o2 > 0; o2 >>= 1, many >>= 1) {
+            for (int many = 16; many > 1; many >>= 1) {
+              const int o2 = many == 16 ? 16 : many / 2;  // lane bits 4, 2, 1 and 0
               const bool high = lane & o2;
 #pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                if (i >= many) break;
+              for (int i = 0; i < many; ++i) {
                 const float give = high ? v[i] : v[i + many], keep = high ? v[i + many] : v[i];
                 v[i] = fmaxf(keep, __shfl_xor_sync(0xffffffffu, give, o2));
               }
             }
-            // rows c + 2 * bits of lane, from 16 rows a step of lane bit 3
-            const int row = c + ((lane >> 3) & 1) * 16 + ((lane >> 2) & 1) * 8 + ((lane >> 1) & 1) * 4 + (lane & 1) * 2;
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-              for (int r = 0; r < 2; ++r)
-                asm volatile("red.relaxed.cluster.shared::cluster.max.u32 [%0], %1;" ::"r"(
-                                 to[r] + (uint32_t)((upper ? kTileN : 0) + row + i) * 4u),
-                             "r"(__float_as_uint(v[i]))
-                             : "memory");
+            const int row = c + (lane >> 4) * 16 + (lane & 7) * 2;  // its two rows
+            *reinterpret_cast<float2*>(part + (quarter * 2 + (upper ? 1 : 0)) * kTileN + row) = make_float2(v[0], v[1]);
+          }
+          epilogue_sync();
+          const uint32_t theirs = in_block(most, rank ^ 1);
+          for (int i = quarter * 32 + lane; i < 2 * kTileN; i += 128) {
+            const float a = fmaxf(fmaxf(part[i], part[i + 2 * kTileN]), fmaxf(part[i + 4 * kTileN], part[i + 6 * kTileN]));
+            most[rank * 2 * kTileN + i] = a;
+            asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(theirs + (rank * 2 * kTileN + (uint32_t)i) * 4u), "f"(a)
+                         : "memory");
           }
           __syncwarp();
           if (lane < 2) arrive_at(in_block(&sm.most_full, (uint32_t)lane));
-          ok = epilogue_agrees(warp_wait(&sm.most_full, (uint32_t)(acc & 1), wait_ns));
+          ok = epilogue_agrees(warp_wait_cluster(&sm.most_full, (uint32_t)(acc & 1), wait_ns));
           if (!ok) break;
           const int groups = (N + 127) / 128;
           for (int i = quarter * 32 + lane; i < 2 * kTileN; i += 128) {
             const int r = i % kTileN, h = i / kTileN;
-            const float a = fmaxf(most[i], 1e-4f);
+            const float a = fmaxf(fmaxf(most[i], most[i + 2 * kTileN]), 1e-4f);
             scale_up[i] = __fdiv_rn(448.0f, a);
-            most[i] = 0.0f;  // for the tile after the next
-            if (rank == 0 && r < valid)
+            if ((int)rank == h && r < valid)
               p.scales[((int64_t)o.lo + o.n0 + r) * 2 * groups + h * groups + o.f0 / 128] = __fdiv_rn(a, 448.0f);
           }
           epilogue_sync();
         }
         for (int c = 0; c < o.n; c += kChunk, ++chunks) {
+          // features to rows through shared memory; what a warp reads here was
+          // written by all four, and the other buffer is free once all four
+          // have come here again
           uint8_t* buf = leaving + (chunks & 1) * kChunkBytes;
           float v[32];
           tmem_load32(src + c, v);
@@ -609,35 +661,31 @@ __global__ void __launch_bounds__(kExpertThreads, 1)
             for (int i = 0; i < 32; ++i)
               reinterpret_cast<uint16_t*>(buf + i * 256)[here] = (uint16_t)pack_bf16x2_rn(v[i], 0.0f);
           }
-          fence_proxy_async_smem();
-          // the copies out of the other buffer have been read; everybody has
-          // written this one
-          if (quarter == 0) bulk_wait_read_all();
           epilogue_sync();
-          if (quarter == 0 && c + lane < valid && nf > 0) {
-            const int64_t row = (int64_t)o.lo + o.n0 + c + lane;
-            const uint8_t* from = buf + lane * 256;
-            bulk_store_s2g(p.out + (row * features + f) * 2, from, (uint32_t)nf * 2u);
-            if (codes16) {
-              bulk_store_s2g(p.ckpt + row * 2 * N + f, from + 128, (uint32_t)nf);
-              bulk_store_s2g(p.ckpt + row * 2 * N + N + f, from + 192, (uint32_t)nf);
-            }
-            bulk_commit();
-          }
-          if (MODE == kGlu && p.ckpt && !codes16) {
-            // rows of codes that start at 8 bytes
-            for (int i = quarter * 32 + lane; i < kChunk * 16; i += 128) {
-              const int r = i / 16, piece = i % 16;  // 8 pieces of gate, 8 of up
-              const int at = piece % 8 * 8;
-              if (c + r < valid && at < nf) {
-                const int64_t row = (int64_t)o.lo + o.n0 + c + r;
-                *reinterpret_cast<uint2*>(p.ckpt + row * 2 * N + piece / 8 * N + f + at) =
-                    *reinterpret_cast<const uint2*>(buf + r * 256 + 128 + piece * 8);
+          const int64_t row0 = (int64_t)o.lo + o.n0 + c;
+          const int many = min(valid - c, kChunk);
+          if (MODE == kGlu) {
+            for (int i = quarter * 32 + lane; i < kChunk * 8; i += 128) {
+              const int r = i / 8, at = i % 8 * 8;  // 8 features
+              if (r >= many || at >= nf) continue;
+              const uint8_t* from = buf + r * 256;
+              st_v4(p.out + ((row0 + r) * N + f + at) * 2, *reinterpret_cast<const uint4*>(from + at * 2));
+              if (p.ckpt) {
+                uint8_t* to = p.ckpt + (row0 + r) * 2 * N + f + at;
+                *reinterpret_cast<uint2*>(to) = *reinterpret_cast<const uint2*>(from + 128 + at);
+                *reinterpret_cast<uint2*>(to + N) = *reinterpret_cast<const uint2*>(from + 192 + at);
               }
             }
-            epilogue_sync();
+          } else {
+#pragma unroll
+            for (int j = 0; j < kChunk * 16 / 128; ++j) {
+              const int i = j * 128 + quarter * 32 + lane, r = i / 16, at = i % 16 * 8;
+              if (r < many && at < nf)
+                st_v4(p.out + ((row0 + r) * features + f + at) * 2, *reinterpret_cast<const uint4*>(buf + r * 256 + at * 2));
+            }
           }
         }
+        if (MODE == kGlu && p.ckpt) epilogue_sync();  // the partial maxima of the next tile go where rows were read
       }
       if (some) {
         tmem_fence_before();
@@ -693,6 +741,20 @@ bool make_map(CUtensorMap* map, const void* base, int64_t width, int64_t rows, i
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// w [E][2F][K] as [E][F / 8][gate, up][8][K], in boxes of 64 gate features, 8
+// by 8 in turn with their up features.
+bool make_glu_map(CUtensorMap* map, const void* base, int64_t K, int64_t F, int64_t E) {
+  const EncodeTiled fn = encode_tiled();
+  if (!fn) return false;
+  const cuuint64_t k = (cuuint64_t)K * 2, f = (cuuint64_t)F;
+  const cuuint64_t dims[5] = {(cuuint64_t)K, 8, 2, f / 8, (cuuint64_t)E};
+  const cuuint64_t strides[4] = {k, f * k, 8 * k, 2 * f * k};
+  const cuuint32_t box[5] = {64, 8, 2, 8, 1}, one[5] = {1, 1, 1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(base), dims, strides, box, one,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // The pairs that can be resident at once on the current device, looked up once
 // per device and kernel.
 template <int MODE>
@@ -735,7 +797,7 @@ cudaError_t launch(const ExpertParams& p, cudaStream_t s) {
          make_map(&maps.out, p.out, K, N, E, K, 32, f32);
   } else {
     if (MODE == kForward) ok = make_map(&maps.a, p.w, K, N, E, K, kHalfM);
-    if (MODE == kGlu) ok = make_map(&maps.a, p.w, K, 2 * N, E, K, 16);
+    if (MODE == kGlu) ok = make_glu_map(&maps.a, p.w, K, N, E);
     if (MODE == kGradInput) ok = make_map(&maps.a, p.w, K, N, E, K, kTileK);
     const int64_t width = MODE == kGradInput ? N : K, stride = MODE == kGradInput ? N : p.x_stride;
     for (int i = 0; i < 4; ++i) ok = ok && make_map(&maps.b[i], p.x, width, p.rows, 0, stride, 16 << i);

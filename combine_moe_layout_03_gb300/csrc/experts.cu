@@ -16,9 +16,10 @@
 // per 128 x 256 x 64 products through L2 and shared memory, which is what a
 // single block with a tile of that size (48 KB) is bound by.
 //
-// Warp 0 loads with TMA (128-byte swizzle) into six stages; warp 1 of the even
-// block issues tcgen05.mma (bf16 in, fp32 accumulators in tensor memory) for
-// both; warps 2-5 of each block store what is finished. Tensor memory holds
+// Warps 0 and 6 load features and rows with TMA (128-byte swizzle) into five
+// or six stages; warp 1 of the even block issues tcgen05.mma (bf16 in, fp32
+// accumulators in tensor memory) for both; warps 2-5 of each block store what
+// is finished. Tensor memory holds
 // two accumulators of 256 columns, so a tile's epilogue runs while the next
 // one is multiplied. The forward product's operands are stored along the
 // reduction (K-major); the gradients read the same buffers across it
@@ -42,12 +43,16 @@ enum { kForward = 0, kGlu = 1, kGradInput = 2, kGradWeight = 3 };
 constexpr int kTileM = 256, kTileN = 256, kTileK = 64;  // of a pair
 constexpr int kHalfM = 128;                             // of a block
 constexpr int kBytesA = kHalfM * kTileK * 2, kBytesB = kTileN / 2 * kTileK * 2;
-constexpr int kStages = 6;
-constexpr int kExpertThreads = 192;
+constexpr int kMaxStages = 6;
+constexpr int kExpertThreads = 224;
 constexpr int kTmemColumns = 512;
 constexpr int kChunk = 32;                   // rows that cross shared memory together
 constexpr int kChunkBytes = kChunk * 256;    // a row's part: 128 features in bf16, or 64 and their codes
 constexpr int kBoxBytes = 4096;              // 32 rows of 128 bytes of dw
+constexpr int kBoxes = 4;                    // of each warp, under way at one time
+// A weight gradient's tile is short (a step per 64 rows of an expert) and its
+// result large, so it has more room for what leaves and a stage less.
+constexpr int stages_of(int mode) { return mode == kGradWeight ? 5 : 6; }
 
 __device__ int32_t g_expert_status;  // MOE_OK, or MOE_ERR_TIMEOUT once a wait gave up
 
@@ -76,8 +81,17 @@ __device__ __forceinline__ uint32_t in_block(const void* p, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
   return a;
 }
+// What this thread wrote is visible to whoever waits with wait_cluster.
 __device__ __forceinline__ void arrive_at(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// For tensor memory that has been read (tmem_fence_before stands before it):
+// no memory is handed over, and none is waited for.
+__device__ __forceinline__ void arrive_read_at(uint32_t bar, uint32_t on) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %1, 0;\n\t@p mbarrier.arrive.shared::cluster.b64 _, [%0];\n\t}" ::"r"(bar),
+      "r"(on)
+      : "memory");
 }
 // Announces copies; it orders nothing else, and a release here would wait for
 // all that the thread has under way, at every step.
@@ -176,9 +190,9 @@ __device__ __forceinline__ void tma_add_3d(const CUtensorMap* map, const void* s
       "r"(x), "r"(y), "r"(z), "r"(smem_u32(src)), "r"(on)
       : "memory");
 }
-// At most one of this thread's groups of bulk stores still reads shared memory.
-__device__ __forceinline__ void bulk_wait_read_one() {
-  asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+// All but the last kBoxes - 1 of this thread's groups of bulk stores have read shared memory.
+__device__ __forceinline__ void bulk_wait_read_boxes() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kBoxes - 1) : "memory");
 }
 __device__ __forceinline__ void tmem_alloc(uint32_t* dst, uint32_t columns) {
   asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst)), "r"(columns)
@@ -256,7 +270,7 @@ struct Tile {
 };
 
 struct ExpertControl {
-  uint64_t full[kStages], empty[kStages], tail[kStages], acc_full[2], acc_empty[2], most_full;
+  uint64_t full[kMaxStages], empty[kMaxStages], tail[kMaxStages], acc_full[2], acc_empty[2], most_full;
   uint32_t tmem;
 };
 // Shared memory behind the stages: what leaves, the control block, and
@@ -265,15 +279,16 @@ struct ExpertControl {
 //           warps pass through the room of what leaves);
 //   all row products: the tiles before each expert.
 constexpr size_t kStageBytes = kBytesA + kBytesB;
-constexpr size_t leaving_bytes(int mode) { return mode == kGradWeight ? 8 * kBoxBytes : 2 * kChunkBytes; }
+constexpr size_t leaving_bytes(int mode) { return mode == kGradWeight ? 4 * kBoxes * kBoxBytes : 2 * kChunkBytes; }
 constexpr size_t glu_bytes(int mode) { return mode == kGlu ? (size_t)5 * 2 * kTileN * 4 : 0; }
 constexpr size_t expert_smem(int mode, int experts) {
-  return 1024 + kStages * kStageBytes + leaving_bytes(mode) + glu_bytes(mode) +
+  return 1024 + stages_of(mode) * kStageBytes + leaving_bytes(mode) + glu_bytes(mode) +
          (mode == kGradWeight ? 0 : ((size_t)experts + 1) * 4) + sizeof(ExpertControl) + 16;
 }
 
+template <int STAGES>
 __device__ __forceinline__ void next_stage(int& st, uint32_t& phase) {
-  if (++st == kStages) {
+  if (++st == STAGES) {
     st = 0;
     phase ^= 1u;
   }
@@ -304,6 +319,7 @@ __device__ __forceinline__ uint4 pack_bf16x8(const float* v) {
 template <int MODE>
 __global__ void __launch_bounds__(kExpertThreads, 1)
     k_expert(ExpertParams p, const __grid_constant__ ExpertMaps maps, uint64_t wait_ns) {
+  constexpr int kStages = stages_of(MODE);
   extern __shared__ uint8_t expert_raw[];
   uint8_t* stages = reinterpret_cast<uint8_t*>(((uintptr_t)expert_raw + 1023) & ~(uintptr_t)1023);
   uint8_t* leaving = stages + kStages * kStageBytes;
@@ -313,13 +329,13 @@ __global__ void __launch_bounds__(kExpertThreads, 1)
   const int warp = threadIdx.x >> 5, lane = (int)lane_id();
   const int E = p.num_experts, K = p.in_features, N = p.out_features;
   const uint32_t rank = cluster_rank();
-  const int64_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(&sm.full[i], 2);   // at the even block: both producers (and their bytes)
+      mbar_init(&sm.full[i], 4);   // at the even block: both blocks' producers (and their bytes)
       mbar_init(&sm.empty[i], 1);
-      mbar_init(&sm.tail[i], 1);
+      mbar_init(&sm.tail[i], 2);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.acc_full[i], 1);
@@ -359,28 +375,28 @@ __global__ void __launch_bounds__(kExpertThreads, 1)
   const int tile_features = MODE == kGlu ? kTileM / 2 : kTileM;
   const int across = (features + tile_features - 1) / tile_features;
   const int down = (K + kTileN - 1) / kTileN;  // weight gradient: column tiles
-  const int64_t num_tiles = MODE == kGradWeight ? (int64_t)E * across * down : (int64_t)first[E] * across;
-  auto find = [&](int64_t t, int& e) {  // e: the expert of this warp's last tile
-    Tile o;
+  const int num_tiles = MODE == kGradWeight ? E * across * down : first[E] * across;
+  // The t-th tile; o is this warp's tile before, or has e = -1.
+  auto find = [&](int t, Tile& o) {
+    const int before = o.e;
     if (MODE == kGradWeight) {
-      e = (int)(t / (across * down));
-      const int i = (int)(t % (across * down));
+      o.e = t / (across * down);
+      const int i = t - o.e * (across * down);
       o.f0 = i / down * tile_features;
       o.n0 = i % down * kTileN;
       o.n = kTileN;
-      o.rows = rows_of(e, o.lo);
+      if (o.e != before) o.rows = rows_of(o.e, o.lo);
     } else {
-      while (t >= (int64_t)first[e + 1] * across) ++e;
-      const int many = first[e + 1] - first[e];
-      const int i = (int)(t - (int64_t)first[e] * across);
+      o.e = max(o.e, 0);
+      while (t >= first[o.e + 1] * across) ++o.e;
+      if (o.e != before) o.rows = rows_of(o.e, o.lo);
+      const int many = first[o.e + 1] - first[o.e];
+      const int i = t - first[o.e] * across;
       o.f0 = i / many * tile_features;
-      o.rows = rows_of(e, o.lo);
       const int width = ((o.rows + many - 1) / many + 31) / 32 * 32;
       o.n0 = i % many * width;
       o.n = min(width, (max(o.rows - o.n0, 0) + 31) / 32 * 32);
     }
-    o.e = e;
-    return o;
   };
   auto steps_of = [&](const Tile& t) {
     const int red = MODE == kGradWeight ? t.rows : MODE == kGradInput ? N : K;
@@ -388,60 +404,57 @@ __global__ void __launch_bounds__(kExpertThreads, 1)
   };
   bool ok = true;
 
-  if (warp == 0) {  // this block's operands into shared memory
+  if (warp == 0 || warp == 6) {  // this block's features, and its rows, into shared memory
+    const bool second = warp == 6;
     const uint32_t on = elect_one();
     const uint32_t full0 = in_block(&sm.full[0], 0), tail0 = in_block(&sm.tail[0], rank);
-    int e = 0, st = 0;
+    Tile o;
+    o.e = -1;
+    int st = 0;
     uint32_t phase = 1;  // a fresh barrier's phase before the first counts as complete
-    for (int64_t t = pair; ok && t < num_tiles; t += pairs) {
-      const Tile o = find(t, e);
+    for (int t = pair; ok && t < num_tiles; t += pairs) {
+      find(t, o);
       const int steps = steps_of(o);
       const int half = o.n / 2;
       // the boxes of this block's half: 16 << i rows each, the largest first,
       // two at most; rather than three, one that brings rows of no use
       int sizes = half / 16;
       if (__popc(sizes) > 2) sizes = 8;
-      const uint32_t bytes_b = (uint32_t)sizes * 16 * kTileK * 2;
+      const uint32_t bytes = !second || MODE == kGradWeight ? kBytesA : (uint32_t)sizes * 16 * kTileK * 2;
+      const int big = 31 - __clz(max(sizes, 1)), small = sizes & ~(1 << big);
+      const CUtensorMap* map = &maps.a;
+      if (second) map = &maps.b[MODE == kGradWeight ? 0 : big];
+      const CUtensorMap* map2 = &maps.b[small ? 31 - __clz(small) : 0];
+      const int feature = o.f0 + (int)rank * kHalfM;
+      const int row = MODE == kGradWeight ? o.n0 + (int)rank * kHalfM : o.lo + o.n0 + (int)rank * half;
       for (int k = 0; k < steps; ++k) {
         if (!warp_wait(&sm.empty[st], phase, wait_ns)) {
           ok = false;
           break;
         }
-        uint8_t* a = stages + st * kStageBytes;
-        uint8_t* b = a + kBytesA;
+        uint8_t* to = stages + st * kStageBytes + (second ? kBytesA : 0);
         const int k0 = k * kTileK;
         uint32_t bar = full0 + 8u * st;
+        // a last step with rows of others goes through the zeroing below
+        if (MODE == kGradWeight && o.rows - k0 < kTileK) bar = tail0 + 8u * st;
+        arrive_expect_at(bar, bytes, on);
         if (MODE == kGradWeight) {
-          // a last step with rows of others goes through the zeroing below
-          if (o.rows - k0 < kTileK) bar = tail0 + 8u * st;
-          arrive_expect_at(bar, kBytesA + kBytesB, on);
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            tma_load_2d(a + i * 8192, &maps.a, o.f0 + (int)rank * kHalfM + i * 64, o.lo + k0, bar, on);
-            tma_load_2d(b + i * 8192, &maps.b[0], o.n0 + (int)rank * kHalfM + i * 64, o.lo + k0, bar, on);
-          }
+          for (int i = 0; i < 2; ++i)
+            tma_load_2d(to + i * 8192, map, (second ? row : feature) + i * 64, o.lo + k0, bar, on);
+        } else if (second) {
+          tma_load_2d(to, map, k0, row, bar, on);
+          if (small) tma_load_2d(to + (16 << big) * 128, map2, k0, row + (16 << big), bar, on);
+        } else if (MODE == kForward) {
+          tma_load_3d(to, &maps.a, k0, feature, o.e, bar, on);
+        } else if (MODE == kGlu) {
+          // 8 features of gate, the same 8 of up, and so on
+          tma_load_5d(to, &maps.a, k0, 0, 0, o.f0 / 8 + (int)rank * 8, o.e, bar, on);
         } else {
-          arrive_expect_at(bar, kBytesA + bytes_b, on);
-          if (MODE == kForward) {
-            tma_load_3d(a, &maps.a, k0, o.f0 + (int)rank * kHalfM, o.e, bar, on);
-          } else if (MODE == kGlu) {
-            // 8 features of gate, the same 8 of up, and so on
-            tma_load_5d(a, &maps.a, k0, 0, 0, o.f0 / 8 + (int)rank * 8, o.e, bar, on);
-          } else {
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-              tma_load_3d(a + i * 8192, &maps.a, o.f0 + (int)rank * kHalfM + i * 64, k0, o.e, bar, on);
-          }
-          const int row = o.lo + o.n0 + (int)rank * half;
-          int at = 0;
-#pragma unroll
-          for (int i = 3; i >= 0; --i)
-            if (sizes & (1 << i)) {
-              tma_load_2d(b + at * 128, &maps.b[i], k0, row + at, bar, on);
-              at += 16 << i;
-            }
+          for (int i = 0; i < 2; ++i) tma_load_3d(to + i * 8192, &maps.a, feature + i * 64, k0, o.e, bar, on);
         }
-        next_stage(st, phase);
+        next_stage<kStages>(st, phase);
       }
     }
     if (!ok) {
@@ -454,24 +467,26 @@ __global__ void __launch_bounds__(kExpertThreads, 1)
     }
   } else if (warp == 1) {  // tensor cores, for both blocks
     constexpr bool a_mn = MODE == kGradInput || MODE == kGradWeight, b_mn = MODE == kGradWeight;
-    int e = 0, st = 0, last = -1;  // last: the stage of the last MMAs, and its phase
+    Tile o;
+    o.e = -1;
+    int st = 0, last = -1;  // last: the stage of the last MMAs, and its phase
     uint32_t phase = 0, last_phase = 0;
     const uint32_t on = elect_one();
     int acc = 0;             // accumulators begun
     uint32_t tail_bits = 0;  // parity of each stage's tail barrier
-    for (int64_t t = pair; ok && t < num_tiles; t += pairs) {
-      const Tile o = find(t, e);
+    for (int t = pair; ok && t < num_tiles; t += pairs) {
+      find(t, o);
       const int steps = steps_of(o);
       if (steps == 0) continue;
       const int as = acc & 1;
-      if (rank == 0 && acc >= 2 && !warp_wait_cluster(&sm.acc_empty[as], (uint32_t)((acc / 2 + 1) & 1), wait_ns)) {
+      if (rank == 0 && acc >= 2 && !warp_wait(&sm.acc_empty[as], (uint32_t)((acc / 2 + 1) & 1), wait_ns)) {
         ok = false;
         break;
       }
       if (MODE != kGradWeight && rank != 0) break;  // nothing to do in the odd block
       tmem_fence_after();
       const uint32_t idesc = instr_desc(a_mn, b_mn, o.n);
-      for (int k = 0; k < steps; ++k, next_stage(st, phase)) {
+      for (int k = 0; k < steps; ++k, next_stage<kStages>(st, phase)) {
         uint8_t* a = stages + st * kStageBytes;
         int parts = kTileK / 16;
         bool zeroed = false;
@@ -492,7 +507,7 @@ __global__ void __launch_bounds__(kExpertThreads, 1)
               *reinterpret_cast<uint4*>(a + c * 8192 + left * 128 + i * 16) = make_uint4(0, 0, 0, 0);
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) arrive_at(in_block(&sm.full[st], 0));
+          if (lane < 2) arrive_at(in_block(&sm.full[st], 0));  // for this block's two producers
         }
         if (rank != 0) continue;
         // a zeroed stage was written by both blocks' warps
@@ -503,11 +518,15 @@ __global__ void __launch_bounds__(kExpertThreads, 1)
         }
         tmem_fence_after();
         const uint64_t da = operand_desc(smem_u32(a), a_mn), db = operand_desc(smem_u32(a + kBytesA), b_mn);
+        if (MODE != kGradWeight || parts == kTileK / 16) {
 #pragma unroll
-        for (int i = 0; i < kTileK / 16; ++i)
-          if (MODE != kGradWeight || i < parts)
+          for (int i = 0; i < kTileK / 16; ++i)
             mma_bf16(tmem + as * kTileN, da + i * (a_mn ? 2048 : 32) / 16, db + i * (b_mn ? 2048 : 32) / 16, idesc,
                      k > 0 || i > 0, on);
+        } else {
+          for (int i = 0; i < parts; ++i)
+            mma_bf16(tmem + as * kTileN, da + i * 2048 / 16, db + i * 2048 / 16, idesc, k > 0 || i > 0, on);
+        }
         mma_commit(&sm.empty[st], on);
         if (k == steps - 1) mma_commit(&sm.acc_full[as], on);
         last = st;
@@ -521,10 +540,12 @@ __global__ void __launch_bounds__(kExpertThreads, 1)
   } else {  // accumulators to memory: warp w reads tensor-memory lanes (w % 4) * 32 ..
     const int quarter = warp & 3;
     const uint32_t on = elect_one();
-    int e = 0;
+    const uint32_t acc_empty0 = in_block(&sm.acc_empty[0], 0);
+    Tile o;
+    o.e = -1;
     int acc = 0, chunks = 0;
-    for (int64_t t = pair; ok && t < num_tiles; t += pairs) {
-      const Tile o = find(t, e);
+    for (int t = pair; ok && t < num_tiles; t += pairs) {
+      find(t, o);
       const bool some = steps_of(o) > 0;  // without rows a weight gradient is zero
       if (!some && MODE != kGradWeight) continue;
       const int as = acc & 1;
@@ -534,16 +555,24 @@ __global__ void __launch_bounds__(kExpertThreads, 1)
         tmem_fence_after();
       }
       const uint32_t src = tmem + (uint32_t)(quarter * 32) * 65536u + (uint32_t)(as * kTileN);
+      // the last columns have been read: the accumulator is free
+      auto release = [&] {
+        tmem_fence_before();
+        __syncwarp();
+        arrive_read_at(acc_empty0 + 8u * as, on);
+      };
       if (MODE == kGradWeight) {
-        // boxes of 32 rows x 128 bytes, each warp its own two buffers
-        uint8_t* mine = leaving + quarter * 2 * kBoxBytes;
+        // boxes of 32 rows x 128 bytes, in each warp's own buffers
+        uint8_t* mine = leaving + quarter * kBoxes * kBoxBytes;
         const bool wide = p.grad_kind != MOE_GRAD_BF16;
         const int step = wide ? 32 : 64;
         const int n = o.f0 + (int)rank * kHalfM + quarter * 32;  // first row of dw
+        const int last = n < N ? min(kTileN, K - o.n0) : 0;  // columns to store
+        if (some && last <= 0) release();
         if (some || p.grad_kind != MOE_GRAD_F32_ADD)
-          for (int c = 0; c < kTileN && o.n0 + c < K && n < N; c += step, ++chunks) {
-            uint8_t* box = mine + (chunks & 1) * kBoxBytes;
-            if (on) bulk_wait_read_one();
+          for (int c = 0; c < last; c += step, ++chunks) {
+            uint8_t* box = mine + chunks % kBoxes * kBoxBytes;
+            if (on) bulk_wait_read_boxes();
             __syncwarp();
             uint4 q[8];
             auto load = [&](int at, float (&v)[32]) {
@@ -568,6 +597,7 @@ __global__ void __launch_bounds__(kExpertThreads, 1)
 #pragma unroll
               for (int i = 0; i < 4; ++i) q[4 + i] = pack_bf16x8(v + 8 * i);
             }
+            if (some && c + step >= last) release();
 #pragma unroll
             for (int i = 0; i < 8; ++i)  // the swizzle that the box is stored with
               *reinterpret_cast<uint4*>(box + lane * 128 + ((i ^ (lane & 7)) << 4)) = q[i];
@@ -641,6 +671,7 @@ __global__ void __launch_bounds__(kExpertThreads, 1)
           uint8_t* buf = leaving + (chunks & 1) * kChunkBytes;
           float v[32];
           tmem_load32(src + c, v);
+          if (c + kChunk >= o.n) release();
           if (MODE == kGlu) {
             float g[16], u[16];
             pair_up(v, upper, g, u);
@@ -687,12 +718,7 @@ __global__ void __launch_bounds__(kExpertThreads, 1)
         }
         if (MODE == kGlu && p.ckpt) epilogue_sync();  // the partial maxima of the next tile go where rows were read
       }
-      if (some) {
-        tmem_fence_before();
-        __syncwarp();
-        if (lane == 0) arrive_at(in_block(&sm.acc_empty[as], 0));
-        ++acc;
-      }
+      if (some) ++acc;
     }
     if (!ok && lane == 0) g_expert_status = MOE_ERR_TIMEOUT;
     bulk_wait_read_all();

@@ -19,7 +19,8 @@
 // Warps 0 and 6 load features and rows with TMA (128-byte swizzle) into five
 // or six stages; warp 1 of the even block issues tcgen05.mma (bf16 in, fp32
 // accumulators in tensor memory) for both; warps 2-5 of each block store what
-// is finished. Tensor memory holds
+// is finished; warp 7 clears what a ragged reduction must not see. Tensor
+// memory holds
 // two accumulators of 256 columns, so a tile's epilogue runs while the next
 // one is multiplied. The forward product's operands are stored along the
 // reduction (K-major); the gradients read the same buffers across it
@@ -44,12 +45,12 @@ constexpr int kTileM = 256, kTileN = 256, kTileK = 64;  // of a pair
 constexpr int kHalfM = 128;                             // of a block
 constexpr int kBytesA = kHalfM * kTileK * 2, kBytesB = kTileN / 2 * kTileK * 2;
 constexpr int kMaxStages = 6;
-constexpr int kExpertThreads = 224;
+constexpr int kExpertThreads = 256;
 constexpr int kTmemColumns = 512;
 constexpr int kChunk = 32;                   // rows that cross shared memory together
 constexpr int kChunkBytes = kChunk * 256;    // a row's part: 128 features in bf16, or 64 and their codes
 constexpr int kBoxBytes = 4096;              // 32 rows of 128 bytes of dw
-constexpr int kBoxes = 4;                    // of each warp, under way at one time
+constexpr int kBoxes = 4;                    // of each warp: two leave while two are filled
 // A weight gradient's tile is short (a step per 64 rows of an expert) and its
 // result large, so it has more room for what leaves and a stage less.
 constexpr int stages_of(int mode) { return mode == kGradWeight ? 5 : 6; }
@@ -85,9 +86,12 @@ __device__ __forceinline__ uint32_t in_block(const void* p, uint32_t rank) {
 __device__ __forceinline__ void arrive_at(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-// For tensor memory that has been read (tmem_fence_before stands before it):
-// no memory is handed over, and none is waited for.
-__device__ __forceinline__ void arrive_read_at(uint32_t bar, uint32_t on) {
+// Where no memory is handed over for another thread to read: tensor memory
+// that has been read (after tmem_fence_before), or shared memory that this
+// block's tensor core reads next (after fence_proxy_async_smem). A release to
+// the cluster would wait for everything under way: at the end of each ragged
+// reduction that took 165 of 940 us.
+__device__ __forceinline__ void arrive_local_at(uint32_t bar, uint32_t on) {
   asm volatile(
       "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %1, 0;\n\t@p mbarrier.arrive.shared::cluster.b64 _, [%0];\n\t}" ::"r"(bar),
       "r"(on)
@@ -189,10 +193,6 @@ __device__ __forceinline__ void tma_add_3d(const CUtensorMap* map, const void* s
       "@p cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2, %3}], [%4];\n\t}" ::"l"(map),
       "r"(x), "r"(y), "r"(z), "r"(smem_u32(src)), "r"(on)
       : "memory");
-}
-// All but the last kBoxes - 1 of this thread's groups of bulk stores have read shared memory.
-__device__ __forceinline__ void bulk_wait_read_boxes() {
-  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kBoxes - 1) : "memory");
 }
 __device__ __forceinline__ void tmem_alloc(uint32_t* dst, uint32_t columns) {
   asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst)), "r"(columns)
@@ -435,8 +435,8 @@ __global__ void __launch_bounds__(kExpertThreads, 1)
         uint8_t* to = stages + st * kStageBytes + (second ? kBytesA : 0);
         const int k0 = k * kTileK;
         uint32_t bar = full0 + 8u * st;
-        // a last step with rows of others goes through the zeroing below
-        if (MODE == kGradWeight && o.rows - k0 < kTileK) bar = tail0 + 8u * st;
+        // a last step that ends inside 16 rows goes through the zeroing below
+        if (MODE == kGradWeight && o.rows - k0 < kTileK && o.rows % 16) bar = tail0 + 8u * st;
         arrive_expect_at(bar, bytes, on);
         if (MODE == kGradWeight) {
 #pragma unroll
@@ -465,7 +465,39 @@ __global__ void __launch_bounds__(kExpertThreads, 1)
       while (global_timer_ns() - t0 < 2000000ull) {
       }
     }
-  } else if (warp == 1) {  // tensor cores, for both blocks
+  } else if (warp == 7) {
+    // The last 16 rows that a weight gradient multiplies may be in part those
+    // of others: zeros instead, by each block in its own stage and ahead of
+    // the products. (Both operands: what the others hold may not be finite.)
+    if (MODE == kGradWeight) {
+      Tile o;
+      o.e = -1;
+      int64_t begun = 0;
+      uint32_t tail_bits = 0;  // parity of each stage's tail barrier
+      for (int t = pair; ok && t < num_tiles; t += pairs) {
+        find(t, o);
+        begun += steps_of(o);
+        const int left = o.rows % kTileK;
+        if (o.rows % 16 == 0) continue;
+        const int st = (int)((begun - 1) % kStages);
+        if (!warp_wait(&sm.tail[st], (tail_bits >> st) & 1u, wait_ns)) {
+          ok = false;
+          break;
+        }
+        tail_bits ^= 1u << st;
+        uint8_t* a = stages + st * kStageBytes;
+        const int zero = ((left + 15) / 16 * 16 - left) * 8;  // 16-byte pieces per 64 columns
+        for (int i = lane; i < zero; i += 32)
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            *reinterpret_cast<uint4*>(a + c * 8192 + left * 128 + i * 16) = make_uint4(0, 0, 0, 0);
+        fence_proxy_async_smem();
+        __syncwarp();
+        arrive_local_at(in_block(&sm.full[st], 0), lane < 2);  // for this block's two producers
+      }
+      if (!ok && lane == 0) g_expert_status = MOE_ERR_TIMEOUT;
+    }
+  } else if (warp == 1 && rank == 0) {  // tensor cores, for both blocks
     constexpr bool a_mn = MODE == kGradInput || MODE == kGradWeight, b_mn = MODE == kGradWeight;
     Tile o;
     o.e = -1;
@@ -473,43 +505,22 @@ __global__ void __launch_bounds__(kExpertThreads, 1)
     uint32_t phase = 0, last_phase = 0;
     const uint32_t on = elect_one();
     int acc = 0;             // accumulators begun
-    uint32_t tail_bits = 0;  // parity of each stage's tail barrier
     for (int t = pair; ok && t < num_tiles; t += pairs) {
       find(t, o);
       const int steps = steps_of(o);
       if (steps == 0) continue;
       const int as = acc & 1;
-      if (rank == 0 && acc >= 2 && !warp_wait(&sm.acc_empty[as], (uint32_t)((acc / 2 + 1) & 1), wait_ns)) {
+      if (acc >= 2 && !warp_wait(&sm.acc_empty[as], (uint32_t)((acc / 2 + 1) & 1), wait_ns)) {
         ok = false;
         break;
       }
-      if (MODE != kGradWeight && rank != 0) break;  // nothing to do in the odd block
       tmem_fence_after();
       const uint32_t idesc = instr_desc(a_mn, b_mn, o.n);
       for (int k = 0; k < steps; ++k, next_stage<kStages>(st, phase)) {
         uint8_t* a = stages + st * kStageBytes;
         int parts = kTileK / 16;
-        bool zeroed = false;
-        if (MODE == kGradWeight && o.rows - k * kTileK < kTileK) {
-          // the rows after the expert's last belong to others: zeros instead,
-          // up to the next whole step of 16, by each block in its own stage
-          const int left = o.rows - k * kTileK;
-          parts = (left + 15) / 16;
-          zeroed = true;
-          if (!warp_wait(&sm.tail[st], (tail_bits >> st) & 1u, wait_ns)) {
-            ok = false;
-            break;
-          }
-          tail_bits ^= 1u << st;
-          const int zero = (parts * 16 - left) * 8;  // 16-byte pieces per 64 columns
-          for (int i = lane; i < zero; i += 32)
-            for (int c = 0; c < 4; ++c)
-              *reinterpret_cast<uint4*>(a + c * 8192 + left * 128 + i * 16) = make_uint4(0, 0, 0, 0);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane < 2) arrive_at(in_block(&sm.full[st], 0));  // for this block's two producers
-        }
-        if (rank != 0) continue;
+        if (MODE == kGradWeight) parts = min(parts, (o.rows - k * kTileK + 15) / 16);
+        const bool zeroed = MODE == kGradWeight && o.rows - k * kTileK < kTileK && o.rows % 16;
         // a zeroed stage was written by both blocks' warps
         if (!(MODE == kGradWeight && zeroed ? warp_wait_cluster(&sm.full[st], phase, wait_ns)
                                             : warp_wait(&sm.full[st], phase, wait_ns))) {
@@ -537,7 +548,7 @@ __global__ void __launch_bounds__(kExpertThreads, 1)
     if (!ok && lane == 0) g_expert_status = MOE_ERR_TIMEOUT;
     // tensor memory is freed below: wait for the last MMAs, with the full budget
     if (last >= 0) mbar_wait(&sm.empty[last], last_phase);
-  } else {  // accumulators to memory: warp w reads tensor-memory lanes (w % 4) * 32 ..
+  } else if (warp != 1) {  // accumulators to memory: warp w reads tensor-memory lanes (w % 4) * 32 ..
     const int quarter = warp & 3;
     const uint32_t on = elect_one();
     const uint32_t acc_empty0 = in_block(&sm.acc_empty[0], 0);
@@ -559,21 +570,28 @@ __global__ void __launch_bounds__(kExpertThreads, 1)
       auto release = [&] {
         tmem_fence_before();
         __syncwarp();
-        arrive_read_at(acc_empty0 + 8u * as, on);
+        arrive_local_at(acc_empty0 + 8u * as, on);
       };
       if (MODE == kGradWeight) {
-        // boxes of 32 rows x 128 bytes, in each warp's own buffers
+        // Boxes of 32 rows x 128 bytes, two neighbours at a time, from this
+        // warp's own four buffers. (One at a time, DRAM sees 128 bytes of a row
+        // at a time; all four, nothing is filled while they leave: 16384 rows,
+        // 7168 x 4096, 32 experts in fp32 1033, 782 and 775 us with two; with
+        // 64 rows an expert 722 and 550 us.)
         uint8_t* mine = leaving + quarter * kBoxes * kBoxBytes;
         const bool wide = p.grad_kind != MOE_GRAD_BF16;
         const int step = wide ? 32 : 64;
         const int n = o.f0 + (int)rank * kHalfM + quarter * 32;  // first row of dw
-        const int last = n < N ? min(kTileN, K - o.n0) : 0;  // columns to store
-        if (some && last <= 0) release();
-        if (some || p.grad_kind != MOE_GRAD_F32_ADD)
-          for (int c = 0; c < last; c += step, ++chunks) {
-            uint8_t* box = mine + chunks % kBoxes * kBoxBytes;
-            if (on) bulk_wait_read_boxes();
-            __syncwarp();
+        const int last = n < N ? min(kTileN, K - o.n0) : 0;      // columns to store
+        const bool store = some || p.grad_kind != MOE_GRAD_F32_ADD;
+        for (int c0 = 0; store && c0 < last; c0 += 2 * step, ++chunks) {
+          if (on) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+          __syncwarp();
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const int c = c0 + j * step;
+            if (c >= last) break;
+            uint8_t* box = mine + ((chunks & 1) * 2 + j) * kBoxBytes;
             uint4 q[8];
             auto load = [&](int at, float (&v)[32]) {
               if (some) {
@@ -597,18 +615,25 @@ __global__ void __launch_bounds__(kExpertThreads, 1)
 #pragma unroll
               for (int i = 0; i < 4; ++i) q[4 + i] = pack_bf16x8(v + 8 * i);
             }
-            if (some && c + step >= last) release();
 #pragma unroll
             for (int i = 0; i < 8; ++i)  // the swizzle that the box is stored with
               *reinterpret_cast<uint4*>(box + lane * 128 + ((i ^ (lane & 7)) << 4)) = q[i];
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (p.grad_kind == MOE_GRAD_F32_ADD)
-              tma_add_3d(&maps.out, box, o.n0 + c, n, o.e, on);
-            else
-              tma_store_3d(&maps.out, box, o.n0 + c, n, o.e, on);
-            if (on) bulk_commit();
           }
+          if (some && c0 + 2 * step >= last) release();
+          fence_proxy_async_smem();
+          __syncwarp();
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const int c = c0 + j * step;
+            if (c >= last) break;
+            if (p.grad_kind == MOE_GRAD_F32_ADD)
+              tma_add_3d(&maps.out, mine + ((chunks & 1) * 2 + j) * kBoxBytes, o.n0 + c, n, o.e, on);
+            else
+              tma_store_3d(&maps.out, mine + ((chunks & 1) * 2 + j) * kBoxBytes, o.n0 + c, n, o.e, on);
+          }
+          if (on) bulk_commit();
+        }
+        if (some && last <= 0) release();
       } else {
         const int own = MODE == kGlu ? 64 : kHalfM;                // features of this block
         const int f = o.f0 + (int)rank * own;

@@ -140,20 +140,6 @@ __device__ __forceinline__ bool warp_wait_cluster(uint64_t* bar, uint32_t parity
   return __all_sync(0xffffffffu, wait_cluster(bar, parity, limit_ns));
 }
 
-// The four epilogue warps: a barrier, and whether all of them came with yes (a
-// wait that gave up ends the loop in all of them, so that none waits alone).
-__device__ __forceinline__ bool epilogue_agrees(bool yes) {
-  uint32_t all;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\tbarrier.cta.red.and.pred q, 1, 128, p;\n\t"
-      "selp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(all)
-      : "r"((uint32_t)yes)
-      : "memory");
-  return all != 0;
-}
-__device__ __forceinline__ void epilogue_sync() { asm volatile("barrier.cta.sync 1, 128;" ::: "memory"); }
-
 // Box into this block's shared memory; the bytes are counted at bar, in either
 // block of the pair.
 __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, int x, int y, uint32_t bar, uint32_t on) {
@@ -270,7 +256,7 @@ struct Tile {
 };
 
 struct ExpertControl {
-  uint64_t full[kMaxStages], empty[kMaxStages], tail[kMaxStages], acc_full[2], acc_empty[2], most_full;
+  uint64_t full[kMaxStages], empty[kMaxStages], tail[kMaxStages], acc_full[2], acc_empty[2], most_full, epilogue;
   uint32_t tmem;
 };
 // Shared memory behind the stages: what leaves, the control block, and
@@ -342,8 +328,15 @@ __global__ void __launch_bounds__(kExpertThreads, 1)
       mbar_init(&sm.acc_empty[i], 8);  // at the even block: both blocks' epilogue warps
     }
     mbar_init(&sm.most_full, 8);
+    mbar_init(&sm.epilogue, 4);
     mbar_init_fence();
   }
+  __syncthreads();
+  // Tensor memory of a pair is allocated in both blocks, by both. Until they
+  // have met, the other block may not run yet (its SM may still be busy with
+  // the kernel before this one), and an allocation that reaches it then is
+  // lost: both hang.
+  cluster_sync();
   if (warp == 1) tmem_alloc(&sm.tmem, kTmemColumns);
   pdl_wait();
   pdl_trigger();
@@ -555,13 +548,23 @@ __global__ void __launch_bounds__(kExpertThreads, 1)
     Tile o;
     o.e = -1;
     int acc = 0, chunks = 0;
+    uint32_t met = 0;  // parity of the epilogue warps' own barrier
+    // The four warps wait for one another, as every wait here with a limit:
+    // one that gave up elsewhere never comes, and the others give up too.
+    auto together = [&] {
+      __syncwarp();
+      if (on) mbar_arrive(&sm.epilogue);
+      const bool came = warp_wait(&sm.epilogue, met, wait_ns);
+      met ^= 1u;
+      return came;
+    };
     for (int t = pair; ok && t < num_tiles; t += pairs) {
       find(t, o);
       const bool some = steps_of(o) > 0;  // without rows a weight gradient is zero
       if (!some && MODE != kGradWeight) continue;
       const int as = acc & 1;
       if (some) {
-        ok = epilogue_agrees(warp_wait(&sm.acc_full[as], (uint32_t)((acc / 2) & 1), wait_ns));
+        ok = warp_wait(&sm.acc_full[as], (uint32_t)((acc / 2) & 1), wait_ns);
         if (!ok) break;
         tmem_fence_after();
       }
@@ -667,7 +670,8 @@ __global__ void __launch_bounds__(kExpertThreads, 1)
             const int row = c + (lane >> 4) * 16 + (lane & 7) * 2;  // its two rows
             *reinterpret_cast<float2*>(part + (quarter * 2 + (upper ? 1 : 0)) * kTileN + row) = make_float2(v[0], v[1]);
           }
-          epilogue_sync();
+          ok = together();
+          if (!ok) break;
           const uint32_t theirs = in_block(most, rank ^ 1);
           for (int i = quarter * 32 + lane; i < 2 * kTileN; i += 128) {
             const float a = fmaxf(fmaxf(part[i], part[i + 2 * kTileN]), fmaxf(part[i + 4 * kTileN], part[i + 6 * kTileN]));
@@ -677,7 +681,7 @@ __global__ void __launch_bounds__(kExpertThreads, 1)
           }
           __syncwarp();
           if (lane < 2) arrive_at(in_block(&sm.most_full, (uint32_t)lane));
-          ok = epilogue_agrees(warp_wait_cluster(&sm.most_full, (uint32_t)(acc & 1), wait_ns));
+          ok = warp_wait_cluster(&sm.most_full, (uint32_t)(acc & 1), wait_ns);
           if (!ok) break;
           const int groups = (N + 127) / 128;
           for (int i = quarter * 32 + lane; i < 2 * kTileN; i += 128) {
@@ -687,7 +691,8 @@ __global__ void __launch_bounds__(kExpertThreads, 1)
             if ((int)rank == h && r < valid)
               p.scales[((int64_t)o.lo + o.n0 + r) * 2 * groups + h * groups + o.f0 / 128] = __fdiv_rn(a, 448.0f);
           }
-          epilogue_sync();
+          ok = together();
+          if (!ok) break;
         }
         for (int c = 0; c < o.n; c += kChunk, ++chunks) {
           // features to rows through shared memory; what a warp reads here was
@@ -717,7 +722,8 @@ __global__ void __launch_bounds__(kExpertThreads, 1)
             for (int i = 0; i < 32; ++i)
               reinterpret_cast<uint16_t*>(buf + i * 256)[here] = (uint16_t)pack_bf16x2_rn(v[i], 0.0f);
           }
-          epilogue_sync();
+          ok = together();
+          if (!ok) break;
           const int64_t row0 = (int64_t)o.lo + o.n0 + c;
           const int many = min(valid - c, kChunk);
           if (MODE == kGlu) {
@@ -741,7 +747,8 @@ __global__ void __launch_bounds__(kExpertThreads, 1)
             }
           }
         }
-        if (MODE == kGlu && p.ckpt) epilogue_sync();  // the partial maxima of the next tile go where rows were read
+        if (!ok) break;
+        if (MODE == kGlu && p.ckpt) ok = together();  // the partial maxima of the next tile go where rows were read
       }
       if (some) ++acc;
     }
@@ -754,6 +761,8 @@ __global__ void __launch_bounds__(kExpertThreads, 1)
   cluster_sync();
   tmem_fence_after();
   if (warp == 1) tmem_free(tmem, kTmemColumns);
+  __syncwarp();
+  cluster_sync();  // and neither leaves before both have freed theirs
 }
 
 // cuTensorMapEncodeTiled, looked up once (the library links no driver stub).

@@ -214,3 +214,43 @@ def test_same_inputs_same_bits(moe):
     a = moe.moe_expert_product_backward_weight(d, dy, x, begin, end, grad_kind=moe.MOE_GRAD_F32)
     b = moe.moe_expert_product_backward_weight(d, dy, x, begin, end, grad_kind=moe.MOE_GRAD_F32)
     assert torch.equal(a, b)
+
+
+def test_behind_a_kernel_that_fills_the_gpu(moe):
+    # calls queued without a pause: the product's pairs of blocks start while
+    # blocks of the kernel before still hold part of each SM
+    rows, cin, f = 4096, 256, 2048
+    begin, end = ranges([1000, 0, 3001, 95], DEV)
+    x, w = normal(1, rows, cin), normal(2, 4, 2 * f, cin, scale=cin ** -0.5)
+    d, gd = moe.MoeExpertDesc(4, rows, cin, f), moe.MoeGluDesc(rows, f)
+    act = torch.empty(rows, f, dtype=torch.bfloat16, device=DEV)
+    ckpt, scales = moe.swiglu_checkpoint(gd, DEV)
+    da, dgu = normal(3, rows, f), torch.empty(rows, 2 * f, dtype=torch.bfloat16, device=DEV)
+    again = torch.empty_like(act)
+    calls = [moe.prepare_expert_swiglu(d, x, begin, end, w, act, ckpt, scales),
+             moe.prepare_swiglu_backward(gd, ckpt, scales, da, dgu, again)]
+    for call in calls:
+        call()
+    torch.cuda.synchronize()
+    first = [t.clone() for t in (act, ckpt, dgu, again)]
+    for _ in range(100):
+        for call in calls:
+            call()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(first, (act, ckpt, dgu, again)))
+
+
+def test_waits_that_run_out_leave_the_context_usable(moe):
+    begin, end = ranges([300, 129], DEV)
+    x, w = whole(1, 429, 1024), whole(2, 2, 520, 1024)
+    d = moe.MoeExpertDesc(2, 429, 1024, 520)
+    torch.cuda.synchronize()
+    moe.moe_set_wait_limit_ns(1)
+    try:
+        moe.moe_expert_product(d, x, begin, end, w)
+        assert moe.moe_device_status() == moe.MOE_ERR_TIMEOUT
+    finally:
+        moe.moe_set_wait_limit_ns(0)
+    y = moe.moe_expert_product(d, x, begin, end, w)
+    assert moe.moe_device_status() == moe.MOE_OK
+    assert torch.equal(y, product(x, begin, end, w)[0].to(torch.bfloat16))

@@ -16,11 +16,11 @@
 // per 128 x 256 x 64 products through L2 and shared memory, which is what a
 // single block with a tile of that size (48 KB) is bound by.
 //
-// Warps 0 and 6 load features and rows with TMA (128-byte swizzle) into five
+// Warps 0 and 2 load features and rows with TMA (128-byte swizzle) into five
 // or six stages; warp 1 of the even block issues tcgen05.mma (bf16 in, fp32
-// accumulators in tensor memory) for both; warps 2-5 of each block store what
-// is finished; warp 7 clears what a ragged reduction must not see. Tensor
-// memory holds
+// accumulators in tensor memory) for both; warp 3 clears what a ragged
+// reduction must not see; warps 4-11 store what is finished. Tensor memory
+// holds
 // two accumulators of 256 columns, so a tile's epilogue runs while the next
 // one is multiplied. The forward product's operands are stored along the
 // reduction (K-major); the gradients read the same buffers across it
@@ -45,12 +45,13 @@ constexpr int kTileM = 256, kTileN = 256, kTileK = 64;  // of a pair
 constexpr int kHalfM = 128;                             // of a block
 constexpr int kBytesA = kHalfM * kTileK * 2, kBytesB = kTileN / 2 * kTileK * 2;
 constexpr int kMaxStages = 6;
-constexpr int kExpertThreads = 256;
+constexpr int kExpertThreads = 384;
+constexpr int kEpilogueWarps = 8;  // two sets of four, a set covers the 128 features
 constexpr int kTmemColumns = 512;
 constexpr int kChunk = 32;                   // rows that cross shared memory together
 constexpr int kChunkBytes = kChunk * 256;    // a row's part: 128 features in bf16, or 64 and their codes
 constexpr int kBoxBytes = 4096;              // 32 rows of 128 bytes of dw
-constexpr int kBoxes = 4;                    // of each warp: two leave while two are filled
+constexpr int kBoxes = 2;                    // of each warp
 // A weight gradient's tile is short (a step per 64 rows of an expert) and its
 // result large, so it has more room for what leaves and a stage less.
 constexpr int stages_of(int mode) { return mode == kGradWeight ? 5 : 6; }
@@ -138,6 +139,28 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint64
 }
 __device__ __forceinline__ bool warp_wait_cluster(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
   return __all_sync(0xffffffffu, wait_cluster(bar, parity, limit_ns));
+}
+
+// Named barriers of the epilogue warps. They wait without a limit, so whoever
+// comes to one must know that the others do: a wait with a limit is followed
+// by a vote, and one that ran out anywhere ends the loop everywhere. (With
+// mbarriers instead, a tile's epilogue took half as long again.)
+__device__ __forceinline__ void set_sync(int set) {
+  if (set == 0)
+    asm volatile("barrier.cta.sync 1, 128;" ::: "memory");
+  else
+    asm volatile("barrier.cta.sync 2, 128;" ::: "memory");
+}
+__device__ __forceinline__ void epilogue_sync() { asm volatile("barrier.cta.sync 3, 256;" ::: "memory"); }
+__device__ __forceinline__ bool epilogue_agrees(bool yes) {
+  uint32_t all;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\tbarrier.cta.red.and.pred q, 3, 256, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(all)
+      : "r"((uint32_t)yes)
+      : "memory");
+  return all != 0;
 }
 
 // Box into this block's shared memory; the bytes are counted at bar, in either
@@ -256,7 +279,7 @@ struct Tile {
 };
 
 struct ExpertControl {
-  uint64_t full[kMaxStages], empty[kMaxStages], tail[kMaxStages], acc_full[2], acc_empty[2], most_full, epilogue;
+  uint64_t full[kMaxStages], empty[kMaxStages], tail[kMaxStages], acc_full[2], acc_empty[2], most_full;
   uint32_t tmem;
 };
 // Shared memory behind the stages: what leaves, the control block, and
@@ -265,7 +288,7 @@ struct ExpertControl {
 //           warps pass through the room of what leaves);
 //   all row products: the tiles before each expert.
 constexpr size_t kStageBytes = kBytesA + kBytesB;
-constexpr size_t leaving_bytes(int mode) { return mode == kGradWeight ? 4 * kBoxes * kBoxBytes : 2 * kChunkBytes; }
+constexpr size_t leaving_bytes(int mode) { return mode == kGradWeight ? kEpilogueWarps * kBoxes * kBoxBytes : 2 * kChunkBytes; }
 constexpr size_t glu_bytes(int mode) { return mode == kGlu ? (size_t)5 * 2 * kTileN * 4 : 0; }
 constexpr size_t expert_smem(int mode, int experts) {
   return 1024 + stages_of(mode) * kStageBytes + leaving_bytes(mode) + glu_bytes(mode) +
@@ -325,10 +348,9 @@ __global__ void __launch_bounds__(kExpertThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.acc_full[i], 1);
-      mbar_init(&sm.acc_empty[i], 8);  // at the even block: both blocks' epilogue warps
+      mbar_init(&sm.acc_empty[i], 2 * kEpilogueWarps);  // at the even block, from both
     }
-    mbar_init(&sm.most_full, 8);
-    mbar_init(&sm.epilogue, 4);
+    mbar_init(&sm.most_full, 2 * kEpilogueWarps);
     mbar_init_fence();
   }
   __syncthreads();
@@ -397,8 +419,8 @@ __global__ void __launch_bounds__(kExpertThreads, 1)
   };
   bool ok = true;
 
-  if (warp == 0 || warp == 6) {  // this block's features, and its rows, into shared memory
-    const bool second = warp == 6;
+  if (warp == 0 || warp == 2) {  // this block's features, and its rows, into shared memory
+    const bool second = warp == 2;
     const uint32_t on = elect_one();
     const uint32_t full0 = in_block(&sm.full[0], 0), tail0 = in_block(&sm.tail[0], rank);
     Tile o;
@@ -458,7 +480,7 @@ __global__ void __launch_bounds__(kExpertThreads, 1)
       while (global_timer_ns() - t0 < 2000000ull) {
       }
     }
-  } else if (warp == 7) {
+  } else if (warp == 3) {
     // The last 16 rows that a weight gradient multiplies may be in part those
     // of others: zeros instead, by each block in its own stage and ahead of
     // the products. (Both operands: what the others hold may not be finite.)
@@ -541,23 +563,13 @@ __global__ void __launch_bounds__(kExpertThreads, 1)
     if (!ok && lane == 0) g_expert_status = MOE_ERR_TIMEOUT;
     // tensor memory is freed below: wait for the last MMAs, with the full budget
     if (last >= 0) mbar_wait(&sm.empty[last], last_phase);
-  } else if (warp != 1) {  // accumulators to memory: warp w reads tensor-memory lanes (w % 4) * 32 ..
-    const int quarter = warp & 3;
+  } else if (warp >= 4) {  // accumulators to memory: warp w reads tensor-memory lanes (w % 4) * 32 ..
+    const int quarter = warp & 3, set = (warp - 4) >> 2;
     const uint32_t on = elect_one();
     const uint32_t acc_empty0 = in_block(&sm.acc_empty[0], 0);
     Tile o;
     o.e = -1;
-    int acc = 0, chunks = 0;
-    uint32_t met = 0;  // parity of the epilogue warps' own barrier
-    // The four warps wait for one another, as every wait here with a limit:
-    // one that gave up elsewhere never comes, and the others give up too.
-    auto together = [&] {
-      __syncwarp();
-      if (on) mbar_arrive(&sm.epilogue);
-      const bool came = warp_wait(&sm.epilogue, met, wait_ns);
-      met ^= 1u;
-      return came;
-    };
+    int acc = 0;
     for (int t = pair; ok && t < num_tiles; t += pairs) {
       find(t, o);
       const bool some = steps_of(o) > 0;  // without rows a weight gradient is zero
@@ -565,6 +577,7 @@ __global__ void __launch_bounds__(kExpertThreads, 1)
       const int as = acc & 1;
       if (some) {
         ok = warp_wait(&sm.acc_full[as], (uint32_t)((acc / 2) & 1), wait_ns);
+        if (MODE != kGradWeight) ok = epilogue_agrees(ok);
         if (!ok) break;
         tmem_fence_after();
       }
@@ -576,25 +589,26 @@ __global__ void __launch_bounds__(kExpertThreads, 1)
         arrive_local_at(acc_empty0 + 8u * as, on);
       };
       if (MODE == kGradWeight) {
-        // Boxes of 32 rows x 128 bytes, two neighbours at a time, from this
-        // warp's own four buffers. (One at a time, DRAM sees 128 bytes of a row
-        // at a time; all four, nothing is filled while they leave: 16384 rows,
-        // 7168 x 4096, 32 experts in fp32 1033, 782 and 775 us with two; with
-        // 64 rows an expert 722 and 550 us.)
-        uint8_t* mine = leaving + quarter * kBoxes * kBoxBytes;
+        // A set stores half of the columns, each warp in boxes of 32 rows x 128
+        // bytes, two neighbours at a time, so that DRAM sees 256 bytes of a
+        // row at a time. (16384 rows, 7168 x 4096, 32 experts, fp32: boxes one
+        // by one 1033 us, in pairs 785 us. The products without any epilogue
+        // take 462 us, the stores by themselves 620 us; stores of whole
+        // sectors from registers, without shared memory, come to 812 us.)
+        uint8_t* mine = leaving + (warp - 4) * kBoxes * kBoxBytes;
         const bool wide = p.grad_kind != MOE_GRAD_BF16;
         const int step = wide ? 32 : 64;
-        const int n = o.f0 + (int)rank * kHalfM + quarter * 32;  // first row of dw
-        const int last = n < N ? min(kTileN, K - o.n0) : 0;      // columns to store
+        const int n = o.f0 + (int)rank * kHalfM + quarter * 32;                        // first row of dw
+        const int begin = set * kTileN / 2, last = n < N ? min(begin + kTileN / 2, K - o.n0) : 0;  // columns to store
         const bool store = some || p.grad_kind != MOE_GRAD_F32_ADD;
-        for (int c0 = 0; store && c0 < last; c0 += 2 * step, ++chunks) {
-          if (on) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+        for (int c0 = begin; store && c0 < last; c0 += kBoxes * step) {
+          if (on) bulk_wait_read_all();
           __syncwarp();
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
+          for (int j = 0; j < kBoxes; ++j) {
             const int c = c0 + j * step;
             if (c >= last) break;
-            uint8_t* box = mine + ((chunks & 1) * 2 + j) * kBoxBytes;
+            uint8_t* box = mine + j * kBoxBytes;
             uint4 q[8];
             auto load = [&](int at, float (&v)[32]) {
               if (some) {
@@ -622,21 +636,21 @@ __global__ void __launch_bounds__(kExpertThreads, 1)
             for (int i = 0; i < 8; ++i)  // the swizzle that the box is stored with
               *reinterpret_cast<uint4*>(box + lane * 128 + ((i ^ (lane & 7)) << 4)) = q[i];
           }
-          if (some && c0 + 2 * step >= last) release();
+          if (some && c0 + kBoxes * step >= last) release();
           fence_proxy_async_smem();
           __syncwarp();
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
+          for (int j = 0; j < kBoxes; ++j) {
             const int c = c0 + j * step;
             if (c >= last) break;
             if (p.grad_kind == MOE_GRAD_F32_ADD)
-              tma_add_3d(&maps.out, mine + ((chunks & 1) * 2 + j) * kBoxBytes, o.n0 + c, n, o.e, on);
+              tma_add_3d(&maps.out, mine + j * kBoxBytes, o.n0 + c, n, o.e, on);
             else
-              tma_store_3d(&maps.out, mine + ((chunks & 1) * 2 + j) * kBoxBytes, o.n0 + c, n, o.e, on);
+              tma_store_3d(&maps.out, mine + j * kBoxBytes, o.n0 + c, n, o.e, on);
           }
           if (on) bulk_commit();
         }
-        if (some && last <= 0) release();
+        if (some && last <= begin) release();
       } else {
         const int own = MODE == kGlu ? 64 : kHalfM;                // features of this block
         const int f = o.f0 + (int)rank * own;
@@ -652,7 +666,7 @@ __global__ void __launch_bounds__(kExpertThreads, 1)
           // blocks, each of which gives its own to the other
           float* part = reinterpret_cast<float*>(leaving);         // [4 warps][gate, up][row]
           float* most = glu_mem + (acc & 1) * 2 * 2 * kTileN;      // [block][gate, up][row]
-          for (int c = 0; c < o.n; c += kChunk) {
+          for (int c = set * kChunk; c < o.n; c += 2 * kChunk) {
             float v[32];
             tmem_load32(src + c, v);
 #pragma unroll
@@ -670,10 +684,9 @@ __global__ void __launch_bounds__(kExpertThreads, 1)
             const int row = c + (lane >> 4) * 16 + (lane & 7) * 2;  // its two rows
             *reinterpret_cast<float2*>(part + (quarter * 2 + (upper ? 1 : 0)) * kTileN + row) = make_float2(v[0], v[1]);
           }
-          ok = together();
-          if (!ok) break;
+          epilogue_sync();
           const uint32_t theirs = in_block(most, rank ^ 1);
-          for (int i = quarter * 32 + lane; i < 2 * kTileN; i += 128) {
+          for (int i = set * 128 + quarter * 32 + lane; i < 2 * kTileN; i += 256) {
             const float a = fmaxf(fmaxf(part[i], part[i + 2 * kTileN]), fmaxf(part[i + 4 * kTileN], part[i + 6 * kTileN]));
             most[rank * 2 * kTileN + i] = a;
             asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(theirs + (rank * 2 * kTileN + (uint32_t)i) * 4u), "f"(a)
@@ -681,27 +694,26 @@ __global__ void __launch_bounds__(kExpertThreads, 1)
           }
           __syncwarp();
           if (lane < 2) arrive_at(in_block(&sm.most_full, (uint32_t)lane));
-          ok = warp_wait_cluster(&sm.most_full, (uint32_t)(acc & 1), wait_ns);
+          ok = epilogue_agrees(warp_wait_cluster(&sm.most_full, (uint32_t)(acc & 1), wait_ns));
           if (!ok) break;
           const int groups = (N + 127) / 128;
-          for (int i = quarter * 32 + lane; i < 2 * kTileN; i += 128) {
+          for (int i = set * 128 + quarter * 32 + lane; i < 2 * kTileN; i += 256) {
             const int r = i % kTileN, h = i / kTileN;
             const float a = fmaxf(fmaxf(most[i], most[i + 2 * kTileN]), 1e-4f);
             scale_up[i] = __fdiv_rn(448.0f, a);
             if ((int)rank == h && r < valid)
               p.scales[((int64_t)o.lo + o.n0 + r) * 2 * groups + h * groups + o.f0 / 128] = __fdiv_rn(a, 448.0f);
           }
-          ok = together();
-          if (!ok) break;
+          epilogue_sync();
         }
-        for (int c = 0; c < o.n; c += kChunk, ++chunks) {
-          // features to rows through shared memory; what a warp reads here was
-          // written by all four, and the other buffer is free once all four
-          // have come here again
-          uint8_t* buf = leaving + (chunks & 1) * kChunkBytes;
+        uint8_t* buf = leaving + set * kChunkBytes;
+        if (set * kChunk >= o.n) release();
+        for (int c = set * kChunk; c < o.n; c += 2 * kChunk) {
+          // features to rows through the set's shared memory
           float v[32];
           tmem_load32(src + c, v);
-          if (c + kChunk >= o.n) release();
+          if (c + 2 * kChunk >= o.n) release();
+          if (c != set * kChunk) set_sync(set);  // the rows before have been read
           if (MODE == kGlu) {
             float g[16], u[16];
             pair_up(v, upper, g, u);
@@ -722,8 +734,7 @@ __global__ void __launch_bounds__(kExpertThreads, 1)
             for (int i = 0; i < 32; ++i)
               reinterpret_cast<uint16_t*>(buf + i * 256)[here] = (uint16_t)pack_bf16x2_rn(v[i], 0.0f);
           }
-          ok = together();
-          if (!ok) break;
+          set_sync(set);
           const int64_t row0 = (int64_t)o.lo + o.n0 + c;
           const int many = min(valid - c, kChunk);
           if (MODE == kGlu) {
@@ -747,8 +758,6 @@ __global__ void __launch_bounds__(kExpertThreads, 1)
             }
           }
         }
-        if (!ok) break;
-        if (MODE == kGlu && p.ckpt) ok = together();  // the partial maxima of the next tile go where rows were read
       }
       if (some) ++acc;
     }

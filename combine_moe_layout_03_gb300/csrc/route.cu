@@ -75,6 +75,20 @@ constexpr int kNone = (int)0x807fffff;  // ordered(-inf): an expert that is take
 
 __device__ __forceinline__ float warp_max(float v) { return unordered(__reduce_max_sync(kAll, ordered(v))); }
 
+// exp(x) and 1 / x in one instruction each beside the product with log2 e:
+// within 4 units of 2^-24 and the rounding of the argument, and 2 units;
+// results below the normal range are 0.
+__device__ __forceinline__ float quick_exp(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.4426950408889634f));
+  return y;
+}
+__device__ __forceinline__ float quick_inverse(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // The weights of the chosen before the scale, from their logits y (-inf: none):
 // s, or s over its sum. The renormalised ones are taken relative to the
 // largest, so that no sum underflows; a lone expert's is 1 exactly. fall:
@@ -362,7 +376,7 @@ __device__ __forceinline__ FixedPoint range_of(const float (&key)[V]) {
 // V: registers a lane spends on its experts (E <= 32 V). SCORED: keys are
 // computed (bias, or sums of scores by group), else they are the logits.
 template <int V, bool VEC, bool SCORED, bool SOFTMAX>
-__global__ void __launch_bounds__(kRouteWarps * 32, V <= 8 ? 10 : V <= 16 ? 6 : 4)
+__global__ void __launch_bounds__(kRouteWarps * 32, V <= 8 ? 8 : V <= 16 ? 6 : 4)
     k_route(RouteParams p, Grouping groups) {
   pdl_wait();
   pdl_trigger();
@@ -396,9 +410,9 @@ __global__ void __launch_bounds__(kRouteWarps * 32, V <= 8 ? 10 : V <= 16 ? 6 : 
   bool open = false;  // more experts in question than lanes: the whole token in fp64
   if (SCORED) {
     const float inv = SOFTMAX ? __fdividef(1.0f, den) : 0.0f;
-    // In units of 2^-24. sigmoid from __expf: s (1 - s) <= 1/4 of the
-    // exponential's 4 (2 ulp) and of its argument's |x| (x s (1 - s) < 1/4),
-    // the sum 1, the quotient 4. softmax: __expf 4 here and expf 4 in the sum,
+    // In units of 2^-24. sigmoid: s (1 - s) <= 1/4 of the exponential's 4 and
+    // of its argument's |x| (x s (1 - s) < 1/4), the sum 1, the inverse 2, and
+    // room for 3 more. softmax: quick_exp 4 here and expf 4 in the sum,
     // the sum's V + 5 roundings, quotient and product 6, the arguments'
     // roundings 9 (|x - top| exp(x - top) < 0.4, and its mean under the
     // distribution <= ln E < 7).
@@ -421,7 +435,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32, V <= 8 ? 10 : V <= 16 ? 6 : 
     }
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const float v = SOFTMAX ? __expf(x[i] - top) * inv : __fdividef(1.0f, 1.0f + __expf(-x[i]));
+      const float v = SOFTMAX ? quick_exp(x[i] - top) * inv : quick_inverse(1.0f + quick_exp(-x[i]));
       // a bias of NaN or -inf takes the expert out, as the logit does
       key[i] = x[i] > -INFINITY ? fmaxf(v + add[i], -INFINITY) : -INFINITY;
     }

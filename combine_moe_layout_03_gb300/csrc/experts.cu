@@ -353,6 +353,9 @@ __global__ void __launch_bounds__(kExpertThreads, 1)
     mbar_init(&sm.most_full, 2 * kEpilogueWarps);
     mbar_init_fence();
   }
+  if (threadIdx.x >= 32 && threadIdx.x < 32 + (MODE == kGradWeight ? 2 : 5))  // a and b[0 .. 3], for the first copies
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<const CUtensorMap*>(&maps) + (threadIdx.x - 32))
+                 : "memory");
   __syncthreads();
   // Tensor memory of a pair is allocated in both blocks, by both. Until they
   // have met, the other block may not run yet (its SM may still be busy with
@@ -379,8 +382,9 @@ __global__ void __launch_bounds__(kExpertThreads, 1)
     if (lane == 0) first[E] = carry;
   }
   tmem_fence_before();
+  // (The other block's tensor memory is there once its warps 0 and 2, which
+  // pass this barrier too, have arrived at a stage's barrier.)
   __syncthreads();
-  cluster_sync();
   tmem_fence_after();
   const uint32_t tmem = sm.tmem;
 

@@ -27,6 +27,7 @@ namespace moe {
 namespace {
 
 constexpr int kRouteWarps = 4;
+constexpr int kBackwardWarps = 8;  // 16384 tokens: 4.6 us, with four 5.1 us (blocks to start)
 constexpr unsigned kAll = 0xffffffffu;
 constexpr float kUnit = 5.9604645e-8f;  // 2^-24, half a step of fp32
 
@@ -640,10 +641,10 @@ __global__ void __launch_bounds__(kRouteWarps * 32, V <= 8 ? 8 : V <= 16 ? 6 : 4
 // expert, then the whole row in one pass of vector stores. FULL (softmax
 // without renormalisation): every logit has a gradient.
 template <int V, bool VEC, bool SOFTMAX, bool FULL>
-__global__ void __launch_bounds__(kRouteWarps * 32) k_route_backward(RouteParams p, float inv_scale) {
+__global__ void __launch_bounds__(kBackwardWarps * 32) k_route_backward(RouteParams p, float inv_scale) {
   pdl_wait();
   pdl_trigger();
-  __shared__ float s_row[kRouteWarps][V * 32];
+  __shared__ float s_row[kBackwardWarps][V * 32];
   const int lane = (int)lane_id(), warp = threadIdx.x >> 5;
   const int E = p.num_experts;
   // as above, no warp leaves early
@@ -790,7 +791,7 @@ cudaError_t launch_route_backward(const RouteParams& p, cudaStream_t s) {
                    : E <= 256 ? backward_kernel<8>(vec, softmax, full)
                    : E <= 512 ? backward_kernel<16>(vec, softmax, full)
                               : backward_kernel<32>(vec, softmax, full);
-  const int warps = p.num_tokens > 1024 ? kRouteWarps : 1;
+  const int warps = p.num_tokens > 1024 ? kBackwardWarps : 1;
   const unsigned blocks = (unsigned)((p.num_tokens + warps - 1) / warps);
   RouteParams q = p;
   float inv_scale = p.scale != 0.0f ? 1.0f / p.scale : 0.0f;

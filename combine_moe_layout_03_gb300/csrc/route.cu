@@ -402,7 +402,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32, V <= 8 ? 8 : V <= 16 ? 6 : 4
     }
     top = warp_max(top);
 #pragma unroll
-    for (int i = 0; i < V; ++i) den += x[i] > -INFINITY ? expf(x[i] - top) : 0.0f;
+    for (int i = 0; i < V; ++i) den += x[i] > -INFINITY ? quick_exp(x[i] - top) : 0.0f;
     den = warp_sum(den);
   }
 
@@ -413,11 +413,11 @@ __global__ void __launch_bounds__(kRouteWarps * 32, V <= 8 ? 8 : V <= 16 ? 6 : 4
     const float inv = SOFTMAX ? __fdividef(1.0f, den) : 0.0f;
     // In units of 2^-24. sigmoid: s (1 - s) <= 1/4 of the exponential's 4 and
     // of its argument's |x| (x s (1 - s) < 1/4), the sum 1, the inverse 2, and
-    // room for 3 more. softmax: quick_exp 4 here and expf 4 in the sum,
-    // the sum's V + 5 roundings, quotient and product 6, the arguments'
-    // roundings 9 (|x - top| exp(x - top) < 0.4, and its mean under the
-    // distribution <= ln E < 7).
-    err = SOFTMAX ? (V + 28) * kUnit * inv : 8 * kUnit;
+    // room for 3 more. softmax: the exponential 4 here and 4 in the sum, the
+    // sum's V + 5 roundings, quotient and product 6, the arguments' two
+    // roundings 16 (|x - top| exp(x - top) < 0.4 here, and its mean under the
+    // distribution <= ln E < 7 in the sum), and room for 1 more.
+    err = SOFTMAX ? (V + 36) * kUnit * inv : 8 * kUnit;
     float add[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) add[i] = 0.0f;
@@ -671,7 +671,7 @@ __global__ void __launch_bounds__(kBackwardWarps * 32) k_route_backward(RoutePar
     top = warp_max(top);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      x[i] = x[i] > -INFINITY ? expf(x[i] - top) : 0.0f;
+      x[i] = x[i] > -INFINITY ? quick_exp(x[i] - top) : 0.0f;
       den += x[i];
     }
     den = warp_sum(den);

@@ -189,11 +189,13 @@ int moe_layout(const moe_desc_t* desc, const int32_t* topk_idx, int32_t* tokens_
 int moe_layout_status(const void* workspace, int32_t* status, moe_stream_t stream);
 
 /* Status of the kernels that wait on shared-memory barriers (the pipelined
- * combine: expert rows brought into shared memory by bulk copies). Every
+ * combine: expert rows brought into shared memory by bulk copies; and the
+ * experts' products, whose warps and pairs of blocks hand operands and
+ * accumulators to one another). Every
  * such wait is bounded: after 1 s it gives up, the kernel records
  * MOE_ERR_TIMEOUT in a device word of the library and returns, leaving the
  * context usable. No legitimate run reaches that limit, since the copies are
- * reads of the GPU's own memory. *status receives MOE_OK or MOE_ERR_TIMEOUT
+ * reads of the GPU's own memory and the products follow them at once. *status receives MOE_OK or MOE_ERR_TIMEOUT
  * for all launches on the current device since the last call with clear != 0
  * (which resets the word). It synchronises the device; it is not for a hot
  * loop. Errors: INVALID_ARG, CUDA. */
@@ -650,8 +652,9 @@ typedef struct {
  * [rows, 2 * ceil(F/128)] (gate's groups, then up's; both NULL: none). act may
  * be NULL where only the checkpoint is wanted. num_rows (device int32, may be
  * NULL) limits the work to rows below *num_rows, e.g. &expert_offset[E]; the
- * other rows are not touched. Arithmetic is fp32 with one rounding. bf16
- * buffers 16-byte aligned, ckpt 8-byte. Errors: INVALID_ARG, SHAPE, ALIGNMENT,
+ * other rows are not touched. Arithmetic is fp32 with one rounding. An
+ * infinity takes its group of 128 with it in the checkpoint (its scale is
+ * infinite), NaN only itself. bf16 buffers 16-byte aligned, ckpt 8-byte. Errors: INVALID_ARG, SHAPE, ALIGNMENT,
  * CUDA. */
 int moe_swiglu(const moe_glu_desc_t* desc, const int32_t* num_rows, const void* gate_up, void* act, void* ckpt,
                float* ckpt_scales, moe_stream_t stream);

@@ -254,3 +254,28 @@ def test_waits_that_run_out_leave_the_context_usable(moe):
     y = moe.moe_expert_product(d, x, begin, end, w)
     assert moe.moe_device_status() == moe.MOE_OK
     assert torch.equal(y, product(x, begin, end, w)[0].to(torch.bfloat16))
+
+
+def test_beside_other_work_on_another_stream(moe):
+    # blocks of another stream's kernels come and go on the same SMs
+    counts, cin, cout = [300, 0, 129, 71], 512, 768
+    begin, end = ranges(counts, DEV)
+    x, w, dy = whole(1, 500, cin), whole(2, 4, cout, cin), whole(3, 500, cout)
+    d = moe.MoeExpertDesc(4, 500, cin, cout)
+    want = product(x, begin, end, w)[0].to(torch.bfloat16)
+    y = torch.zeros(500, cout, dtype=torch.bfloat16, device=DEV)
+    dw = torch.zeros(4, cout, cin, device=DEV)
+    sums = torch.stack([dy[b:t].double().t() @ x[b:t].double() for b, t in zip(begin.tolist(), end.tolist())]).float()
+    other, mine = torch.cuda.Stream(), torch.cuda.Stream()
+    noise = torch.randn(1 << 22, device=DEV)
+    torch.cuda.synchronize()
+    calls = [moe.prepare_expert_product(d, x, begin, end, w, y, stream=mine),
+             moe.prepare_expert_product_backward_weight(d, dy, x, begin, end, dw, moe.MOE_GRAD_F32, stream=mine)]
+    for _ in range(30):
+        with torch.cuda.stream(other):
+            for _ in range(4):
+                noise.mul_(1.0001)
+        for call in calls:
+            call()
+    torch.cuda.synchronize()
+    assert torch.equal(y, want) and torch.equal(dw, sums)

@@ -34,9 +34,13 @@
 // 256 x 256 tile takes 515 cycles of which 512 are theirs, and then the power
 // cap: 16384 rows x 7168 -> 4096 over 32 experts of 512 take 537 us (1790
 // TFLOP/s) in short runs and 618 us (1556, a library's batched product 614 us)
-// in long ones; experts of 412 to 616 rows 14% more (more tiles of fewer
-// rows). Few rows: the weights, 8 rows an expert 275 us for 1.88 GB (6.8
-// TB/s). Weight gradients: their result, 3.76 GB of fp32 780 us.
+// in long ones. A tile of n rows takes 2 n cycles a step in the tensor cores,
+// and 256 + n for its operands (16 KB of features and 64 n bytes of rows for
+// each SM, at 64 bytes a cycle from L2; measured 452 cycles at 192 rows, 504 at
+// 224): 480 rows an expert 501 to 538 us, 416 rows 492; experts of 412 to 616
+// rows take 670 us in long runs. Few rows: the weights, 8 rows an expert 274
+// us for 1.88 GB (6.9 TB/s). Weight gradients: their result, 3.76 GB of fp32
+// 780 us.
 #include <cuda.h>
 
 #include <mutex>
@@ -400,7 +404,12 @@ __global__ void __launch_bounds__(kExpertThreads, 1)
   const uint32_t tmem = sm.tmem;
 
   // Tiles in order: expert, then features, then rows (columns of dw); pairs
-  // take every pairs-th, so that those running at one time share operands.
+  // take one each in turn, so that those running at one time share operands,
+  // and each second round in the other direction: where wide and narrow tiles
+  // alternate, an even number of pairs would give the wide ones to the same
+  // pairs every time, and pairs that share weights would drift apart (480 rows
+  // an expert: 583 to 607 us for 501 to 538).
+  const int turn = 2 * (pairs - pair) - 1;
   const int features = MODE == kGradInput ? K : N;
   const int tile_features = MODE == kGlu ? kTileM / 2 : kTileM;
   const int across = (features + tile_features - 1) / tile_features;
@@ -442,7 +451,7 @@ __global__ void __launch_bounds__(kExpertThreads, 1)
     o.e = -1;
     int st = 0;
     uint32_t phase = 1;  // a fresh barrier's phase before the first counts as complete
-    for (int t = pair; ok && t < num_tiles; t += pairs) {
+    for (int t = pair, jump = turn; ok && t < num_tiles; t += jump, jump = 2 * pairs - jump) {
       find(t, o);
       const int steps = steps_of(o);
       const int half = o.n / 2;
@@ -504,7 +513,7 @@ __global__ void __launch_bounds__(kExpertThreads, 1)
       o.e = -1;
       int64_t begun = 0;
       uint32_t tail_bits = 0;  // parity of each stage's tail barrier
-      for (int t = pair; ok && t < num_tiles; t += pairs) {
+      for (int t = pair, jump = turn; ok && t < num_tiles; t += jump, jump = 2 * pairs - jump) {
         find(t, o);
         begun += steps_of(o);
         const int left = o.rows % kTileK;
@@ -535,7 +544,7 @@ __global__ void __launch_bounds__(kExpertThreads, 1)
     uint32_t phase = 0, last_phase = 0;
     const uint32_t on = elect_one();
     int acc = 0;             // accumulators begun
-    for (int t = pair; ok && t < num_tiles; t += pairs) {
+    for (int t = pair, jump = turn; ok && t < num_tiles; t += jump, jump = 2 * pairs - jump) {
       find(t, o);
       const int steps = steps_of(o);
       if (steps == 0) continue;
@@ -585,7 +594,7 @@ __global__ void __launch_bounds__(kExpertThreads, 1)
     Tile o;
     o.e = -1;
     int acc = 0;
-    for (int t = pair; ok && t < num_tiles; t += pairs) {
+    for (int t = pair, jump = turn; ok && t < num_tiles; t += jump, jump = 2 * pairs - jump) {
       find(t, o);
       const bool some = steps_of(o) > 0;  // without rows a weight gradient is zero
       if (!some && MODE != kGradWeight) continue;

@@ -409,7 +409,9 @@ __global__ void __launch_bounds__(kExpertThreads, 1)
   // alternate, an even number of pairs would give the wide ones to the same
   // pairs every time, and pairs that share weights would drift apart (480 rows
   // an expert: 583 to 607 us for 501 to 538).
-  const int turn = 2 * (pairs - pair) - 1;
+  // (Tiles of a weight gradient's expert are alike, and neighbours in a round
+  // share columns: there it costs 1%.)
+  const int turn = MODE == kGradWeight ? pairs : 2 * (pairs - pair) - 1;
   const int features = MODE == kGradInput ? K : N;
   const int tile_features = MODE == kGlu ? kTileM / 2 : kTileM;
   const int across = (features + tile_features - 1) / tile_features;

@@ -32,8 +32,8 @@
 // What bounds it (peaks as measured: 6.79 TB/s, 1957 TFLOP/s burst and 1758
 // sustained under the power cap). Many rows: the tensor cores, a step of a
 // 256 x 256 tile takes 515 cycles of which 512 are theirs, and then the power
-// cap: 16384 rows x 7168 -> 4096 over 32 experts of 512 take 537 us (1790
-// TFLOP/s) in short runs and 618 us (1556, a library's batched product 614 us)
+// cap: 16384 rows x 7168 -> 4096 over 32 experts of 512 take 522 us (1840
+// TFLOP/s) in short runs and 573 to 618 us (a library's batched product 614 us)
 // in long ones. A tile of n rows takes 2 n cycles a step in the tensor cores,
 // and 256 + n for its operands (16 KB of features and 64 n bytes of rows for
 // each SM, at 64 bytes a cycle from L2; measured 452 cycles at 192 rows, 504 at

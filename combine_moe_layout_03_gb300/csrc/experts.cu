@@ -99,14 +99,25 @@ __device__ __forceinline__ uint32_t in_block(const void* p, uint32_t rank) {
 __device__ __forceinline__ void arrive_at(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-// Where no memory is handed over for another thread to read: tensor memory
-// that has been read (after tmem_fence_before), or shared memory that this
-// block's tensor core reads next (after fence_proxy_async_smem). A release to
-// the cluster would wait for everything under way: at the end of each ragged
-// reduction that took 165 of 940 us.
+// A release to this block alone. To the other block it hands over no memory,
+// only tensor memory that has been read (after tmem_fence_before).
 __device__ __forceinline__ void arrive_local_at(uint32_t bar, uint32_t on) {
   asm volatile(
       "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %1, 0;\n\t@p mbarrier.arrive.shared::cluster.b64 _, [%0];\n\t}" ::"r"(bar),
+      "r"(on)
+      : "memory");
+}
+// What this warp wrote to its block's shared memory is visible to whoever waits
+// with wait_cluster. All lanes come; those with `on` arrive. The fence covers
+// shared memory alone: arrive_at would wait for all that the block has under
+// way, stores to global memory too (at the end of each ragged reduction, 165
+// of 940 us).
+__device__ __forceinline__ void arrive_with_shared_at(uint32_t bar, uint32_t on) {
+  __syncwarp();
+  asm volatile("fence.release.sync_restrict::shared::cta.cluster;" ::: "memory");
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %1, 0;\n\t"
+      "@p mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];\n\t}" ::"r"(bar),
       "r"(on)
       : "memory");
 }
@@ -533,8 +544,8 @@ __global__ void __launch_bounds__(kExpertThreads, 1)
           for (int c = 0; c < 4; ++c)
             *reinterpret_cast<uint4*>(a + c * 8192 + left * 128 + i * 16) = make_uint4(0, 0, 0, 0);
         fence_proxy_async_smem();
-        __syncwarp();
-        arrive_local_at(in_block(&sm.full[st], 0), lane < 2);  // for this block's two producers
+        // for this block's two producers; the even block issues the products
+        arrive_with_shared_at(in_block(&sm.full[st], 0), lane < 2);
       }
       if (!ok && lane == 0) g_expert_status = MOE_ERR_TIMEOUT;
     }

@@ -1,0 +1,44 @@
+"""The experts' products where blocks, warps and ranges meet: ragged ends
+beside rows that are not finite, ranges outside the buffers, waits. Inputs are
+small whole numbers, so every sum is exact (see test_gpu_experts)."""
+import pytest
+import torch
+
+from layer_reference import ranges
+from test_gpu_experts import DEV, whole
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def moe():
+    from combine_moe_layout_03_gb300 import moe as m
+    yield m
+    assert m.moe_device_status() == m.MOE_OK
+
+
+def sums(dy, x, begin, end):
+    return torch.stack([dy[b:t].double().t() @ x[b:t].double() for b, t in zip(begin.tolist(), end.tolist())])
+
+
+@pytest.mark.parametrize("cin,cout", [(520, 264), (1024, 768)])
+def test_ragged_ends_beside_rows_that_are_not_finite(moe, cin, cout):
+    # every second expert's rows are NaN or infinite; the others' reductions end
+    # inside 16 rows that reach into them, in many tiles of every pair of blocks
+    g = torch.Generator().manual_seed(1)
+    counts = [int(torch.randint(1, 200, (), generator=g)) // 16 * 16 + 1 + i % 15 for i in range(64)]
+    begin, end = ranges(counts, DEV)
+    rows = sum(counts)
+    x, dy = whole(1, rows, cin), whole(2, rows, cout)
+    for e in range(1, 64, 2):
+        x[begin[e]:end[e]] = float("nan") if e % 4 == 1 else float("inf")
+        dy[begin[e]:end[e]] = float("inf") if e % 4 == 1 else float("nan")
+    d = moe.MoeExpertDesc(64, rows, cin, cout)
+    want = sums(dy, x, begin, end)[::2]
+    for kind, t in ((moe.MOE_GRAD_F32, torch.float32), (moe.MOE_GRAD_BF16, torch.bfloat16)):
+        dw = torch.empty(64, cout, cin, dtype=t, device=DEV)
+        call = moe.prepare_expert_product_backward_weight(d, dy, x, begin, end, dw, kind)
+        for _ in range(20):
+            dw.fill_(7.0)
+            call()
+            assert torch.equal(dw[::2], want.to(t))

@@ -393,7 +393,7 @@ __global__ void __launch_bounds__(kExpertThreads, 1)
   pdl_trigger();
   auto rows_of = [&](int e, int& lo) {
     lo = max(p.row_begin[e], 0);
-    return max((int)min((int64_t)p.row_end[e], p.rows) - lo, 0);
+    return max((int)min((int64_t)max(p.row_end[e], 0), p.rows) - lo, 0);
   };
   if (MODE != kGradWeight && warp == 0) {
     int carry = 0;

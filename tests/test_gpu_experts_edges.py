@@ -42,3 +42,27 @@ def test_ragged_ends_beside_rows_that_are_not_finite(moe, cin, cout):
             dw.fill_(7.0)
             call()
             assert torch.equal(dw[::2], want.to(t))
+
+
+def test_ranges_that_end_far_below_zero(moe):
+    # such an expert has no rows, whatever its begin is
+    rows, cin, cout, least = 100, 72, 144, -(1 << 31)
+    begin = torch.tensor([5, 0, 99, (1 << 31) - 1, -7], dtype=torch.int32, device=DEV)
+    end = torch.tensor([least, 60, least + 50, least, least + 1], dtype=torch.int32, device=DEV)
+    x, w, dy = whole(1, rows, cin), whole(2, 5, cout, cin), whole(3, rows, cout)
+    d = moe.MoeExpertDesc(5, rows, cin, cout)
+    y = torch.full((rows, cout), 7.0, dtype=torch.bfloat16, device=DEV)
+    moe.moe_expert_product(d, x, begin, end, w, y)
+    assert torch.equal(y[:60], (x[:60].double() @ w[1].double().t()).to(torch.bfloat16)) and bool((y[60:] == 7.0).all())
+    dx = torch.full((rows, cin), 7.0, dtype=torch.bfloat16, device=DEV)
+    moe.moe_expert_product_backward_input(d, dy, begin, end, w, dx)
+    assert torch.equal(dx[:60], (dy[:60].double() @ w[1].double()).to(torch.bfloat16)) and bool((dx[60:] == 7.0).all())
+    dw = moe.moe_expert_product_backward_weight(d, dy, x, begin, end, grad_kind=moe.MOE_GRAD_F32)
+    want = torch.zeros_like(dw)
+    want[1] = (dy[:60].double().t() @ x[:60].double()).float()
+    assert torch.equal(dw, want)
+    act = torch.full((rows, cout // 2), 7.0, dtype=torch.bfloat16, device=DEV)
+    ckpt, scales = moe.swiglu_checkpoint(moe.MoeGluDesc(rows, cout // 2), DEV)
+    scales.fill_(-1.0)
+    moe.moe_expert_swiglu(moe.MoeExpertDesc(5, rows, cin, cout // 2), x, begin, end, w, act, ckpt, scales)
+    assert bool((act[60:] == 7.0).all()) and bool((scales[60:] == -1.0).all()) and bool((scales[:60] > 0).all())

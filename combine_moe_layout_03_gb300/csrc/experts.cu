@@ -164,6 +164,20 @@ __device__ __forceinline__ bool warp_wait_cluster(uint64_t* bar, uint32_t parity
   return __all_sync(0xffffffffu, wait_cluster(bar, parity, limit_ns));
 }
 
+// The same where what is waited for may be as far away as an expert's last row
+// (a weight gradient reduces over all of them): the budget is for one step. It
+// starts again as long as this block's producer has begun steps since.
+__device__ __forceinline__ bool warp_wait_steps(uint64_t* bar, uint32_t parity, uint64_t limit_ns,
+                                                const volatile uint32_t* begun) {
+  uint32_t seen = *begun;
+  while (!warp_wait(bar, parity, limit_ns)) {
+    const uint32_t now = *begun;
+    if (__all_sync(0xffffffffu, now == seen)) return false;
+    seen = now;
+  }
+  return true;
+}
+
 // Named barriers of the epilogue warps. They wait without a limit, so whoever
 // comes to one must know that the others do: a wait with a limit is followed
 // by a vote, and one that ran out anywhere ends the loop everywhere. (With
@@ -307,6 +321,7 @@ struct Tile {
 struct ExpertControl {
   uint64_t full[kMaxStages], empty[kMaxStages], tail[kMaxStages], acc_full[2], acc_empty[2], most_full;
   uint32_t tmem;
+  uint32_t begun;  // weight gradient: steps whose copies this block has asked for
 };
 // Shared memory behind the stages: what leaves, the control block, and
 //   swiglu: the largest magnitudes of gate and up by row, of both blocks and
@@ -377,6 +392,7 @@ __global__ void __launch_bounds__(kExpertThreads, 1)
       mbar_init(&sm.acc_empty[i], 2 * kEpilogueWarps);  // at the even block, from both
     }
     mbar_init(&sm.most_full, 2 * kEpilogueWarps);
+    sm.begun = 0;
     mbar_init_fence();
   }
   if (threadIdx.x >= 32 && threadIdx.x < 32 + (MODE == kGradWeight ? 2 : 5))  // a and b[0 .. 3], for the first copies
@@ -464,6 +480,7 @@ __global__ void __launch_bounds__(kExpertThreads, 1)
     o.e = -1;
     int st = 0;
     uint32_t phase = 1;  // a fresh barrier's phase before the first counts as complete
+    uint32_t begun = 0;
     for (int t = pair, jump = turn; ok && t < num_tiles; t += jump, jump = 2 * pairs - jump) {
       find(t, o);
       const int steps = steps_of(o);
@@ -491,6 +508,8 @@ __global__ void __launch_bounds__(kExpertThreads, 1)
         if (MODE == kGradWeight && o.rows - k0 < kTileK && o.rows % 16) bar = tail0 + 8u * st;
         arrive_expect_at(bar, bytes, on);
         if (MODE == kGradWeight) {
+          ++begun;
+          if (on && !second) *const_cast<volatile uint32_t*>(&sm.begun) = begun;
 #pragma unroll
           for (int i = 0; i < 2; ++i)
             tma_load_2d(to + i * 8192, map, (second ? row : feature) + i * 64, o.lo + k0, bar, on);
@@ -532,7 +551,7 @@ __global__ void __launch_bounds__(kExpertThreads, 1)
         const int left = o.rows % kTileK;
         if (o.rows % 16 == 0) continue;
         const int st = (int)((begun - 1) % kStages);
-        if (!warp_wait(&sm.tail[st], (tail_bits >> st) & 1u, wait_ns)) {
+        if (!warp_wait_steps(&sm.tail[st], (tail_bits >> st) & 1u, wait_ns, &sm.begun)) {
           ok = false;
           break;
         }
@@ -613,8 +632,9 @@ __global__ void __launch_bounds__(kExpertThreads, 1)
       if (!some && MODE != kGradWeight) continue;
       const int as = acc & 1;
       if (some) {
-        ok = warp_wait(&sm.acc_full[as], (uint32_t)((acc / 2) & 1), wait_ns);
-        if (MODE != kGradWeight) ok = epilogue_agrees(ok);
+        const uint32_t parity = (uint32_t)((acc / 2) & 1);
+        ok = MODE == kGradWeight ? warp_wait_steps(&sm.acc_full[as], parity, wait_ns, &sm.begun)
+                                 : epilogue_agrees(warp_wait(&sm.acc_full[as], parity, wait_ns));
         if (!ok) break;
         tmem_fence_after();
       }

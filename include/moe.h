@@ -191,11 +191,12 @@ int moe_layout_status(const void* workspace, int32_t* status, moe_stream_t strea
 /* Status of the kernels that wait on shared-memory barriers (the pipelined
  * combine: expert rows brought into shared memory by bulk copies; and the
  * experts' products, whose warps and pairs of blocks hand operands and
- * accumulators to one another). Every
- * such wait is bounded: after 1 s it gives up, the kernel records
- * MOE_ERR_TIMEOUT in a device word of the library and returns, leaving the
- * context usable. No legitimate run reaches that limit, since the copies are
- * reads of the GPU's own memory and the products follow them at once. *status receives MOE_OK or MOE_ERR_TIMEOUT
+ * accumulators to one another). Every such wait is bounded: after 1 s it gives
+ * up, the kernel records MOE_ERR_TIMEOUT in a device word of the library and
+ * returns, leaving the context usable. No legitimate run reaches that limit,
+ * since the copies are reads of the GPU's own memory and the products follow
+ * them at once; where a weight gradient waits for all rows of an expert, the
+ * second is for 64 rows of them. *status receives MOE_OK or MOE_ERR_TIMEOUT
  * for all launches on the current device since the last call with clear != 0
  * (which resets the word). It synchronises the device; it is not for a hot
  * loop. Errors: INVALID_ARG, CUDA. */

@@ -66,3 +66,24 @@ def test_ranges_that_end_far_below_zero(moe):
     scales.fill_(-1.0)
     moe.moe_expert_swiglu(moe.MoeExpertDesc(5, rows, cin, cout // 2), x, begin, end, w, act, ckpt, scales)
     assert bool((act[60:] == 7.0).all()) and bool((scales[60:] == -1.0).all()) and bool((scales[:60] > 0).all())
+
+
+def test_a_long_reduction_outlasts_the_budget_of_a_wait(moe):
+    # a million rows of one expert take several times the budget; the ragged
+    # expert that the same pair of blocks comes to last waits for two such
+    long, e = 1 << 20, 153
+    counts = [0] * e
+    counts[0] = counts[76] = long
+    counts[152] = 5
+    begin, end = ranges(counts, DEV)
+    x, dy = whole(1, sum(counts), 8), whole(2, sum(counts), 8)
+    dw = torch.full((e, 8, 8), 7.0, device=DEV)
+    want = sums(dy, x, begin, end).float()
+    torch.cuda.synchronize()
+    moe.moe_set_wait_limit_ns(1_000_000)
+    try:
+        moe.moe_expert_product_backward_weight(moe.MoeExpertDesc(e, sum(counts), 8, 8), dy, x, begin, end, dw, moe.MOE_GRAD_F32)
+        assert moe.moe_device_status() == moe.MOE_OK
+    finally:
+        moe.moe_set_wait_limit_ns(0)
+    assert torch.equal(dw, want)

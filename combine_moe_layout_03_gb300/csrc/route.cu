@@ -30,6 +30,7 @@ constexpr int kRouteWarps = 4;
 constexpr int kBackwardWarps = 8;  // 16384 tokens: 4.6 us, with four 5.1 us (blocks to start)
 constexpr unsigned kAll = 0xffffffffu;
 constexpr float kUnit = 5.9604645e-8f;  // 2^-24, half a step of fp32
+constexpr float kLargest = 3.402823466e38f;
 
 __device__ __forceinline__ float raw_logit(const RouteParams& p, int64_t t, int e) {
   const int64_t i = t * p.stride + e;
@@ -37,7 +38,7 @@ __device__ __forceinline__ float raw_logit(const RouteParams& p, int64_t t, int 
                                           : ((const float*)p.logits)[i];
 }
 // NaN goes the way of -inf (fmaxf takes the number), +inf becomes FLT_MAX, -0 becomes +0.
-__device__ __forceinline__ float cleaned(float x) { return fminf(fmaxf(x, -INFINITY), 3.402823466e38f) + 0.0f; }
+__device__ __forceinline__ float cleaned(float x) { return fminf(fmaxf(x, -INFINITY), kLargest) + 0.0f; }
 __device__ __forceinline__ float load_logit(const RouteParams& p, int64_t t, int e) {
   return cleaned(raw_logit(p, t, e));
 }
@@ -498,11 +499,16 @@ __global__ void __launch_bounds__(kRouteWarps * 32, V <= 8 ? 8 : V <= 16 ? 6 : 4
     }
     const int g = lane >> lanes_log;
     const bool head = g << lanes_log == lane && g < G;
+    // Counts and their size stay finite where a key is infinite (a bias that
+    // forces an expert) or two of them overflow, so that the differences below
+    // have a value: such counts are equal here, and fp64 tells them apart.
     float count = a, size = head && a > -INFINITY ? fabsf(a) : 0.0f;
     if (two && b > -INFINITY) {
       count += b;
       size += fabsf(b);
     }
+    if (a > -INFINITY) count = fminf(fmaxf(count, -kLargest), kLargest);
+    size = fminf(size, kLargest);
     const int mark = head ? ordered(count + 0.0f) : INT_MIN;
     int left = mark, m = kNone;
     unsigned keep = 0;

@@ -1,0 +1,59 @@
+"""Keys at the edges of what fp32 can tell: infinite and overflowing biases,
+infinite logits, and near-ties that lie behind the last place. Ids have to be
+those of 64-bit arithmetic (the bounds of weights are those of test_gpu_route)."""
+import numpy as np
+import pytest
+import torch
+
+from test_gpu_route import DEV, INF, check, draw, draw_bias
+
+pytestmark = pytest.mark.gpu
+MOST = torch.finfo(torch.float32).max
+
+
+@pytest.fixture(scope="module")
+def moe():
+    from combine_moe_layout_03_gb300 import moe as m
+    return m
+
+
+# ---- group counts that are infinite or overflow
+
+@pytest.mark.parametrize("group_score", ["max", "top2"])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("e,groups,topk_groups", [(16, 4, 1), (64, 8, 2), (256, 8, 3), (60, 6, 2), (96, 32, 4)])
+def test_infinite_bias_forces_an_expert(moe, e, groups, topk_groups, score, group_score):
+    per = e // groups
+    x = draw(21, 24, e, False)
+    # as many forced groups as are taken, fewer, more, and two experts of one group
+    for forced in ([g * per + 1 for g in range(groups - topk_groups, groups)], [e - 1],
+                   [g * per for g in range(groups)], [e - 1, e - 2, per]):
+        bias = draw_bias(21, e)
+        bias[forced] = INF
+        check(moe, x, bias, 2, score, groups, topk_groups, group_score, grad=False)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("e,groups", [(32, 4), (64, 8), (256, 8), (24, 4)])
+def test_group_sums_that_overflow(moe, e, groups, score):
+    per = e // groups
+    x = draw(22, 16, e, False)
+    bias = draw_bias(22, e)
+    bias[per:per + 2] = 2e38
+    bias[2 * per:2 * per + 2] = 3e38  # the larger sum, in 64 bits
+    for topk_groups in (1, 2, 3):
+        check(moe, x, bias, 4, score, groups, topk_groups, "top2", grad=False)
+    # experts masked by the lowest value stay before those that are taken out
+    bias = draw_bias(22, e)
+    bias[(groups - 1) * per:] = -MOST
+    x[:, :(groups - 2) * per] = -INF
+    check(moe, x, bias, 4, score, groups, 2, "top2", grad=False)
+
+
+@pytest.mark.parametrize("e,groups", [(32, 4), (256, 8), (12, 3)])
+def test_infinite_logits_tie_with_the_largest(moe, e, groups):
+    x = draw(23, 8, e, False)
+    x[:, 1] = MOST
+    x[:, e - 1] = INF
+    for score in ("softmax", "sigmoid"):
+        check(moe, x, None, 2, score, groups, 1, "max", grad=False)

@@ -371,7 +371,9 @@ __device__ __forceinline__ FixedPoint range_of(const float (&key)[V]) {
       if (key[i] >= -kOrdinary) least = fminf(least, key[i]);
   }
   f.lo = fminf(unordered(__reduce_min_sync(kAll, ordered(least))), f.hi);
-  f.per_range = f.hi > f.lo ? __fdividef(0.999999f, f.hi - f.lo) : 0.0f;
+  // (Without a range keys from lo up are one step; not times 0, which would
+  // lose those that are infinite.)
+  f.per_range = f.hi > f.lo ? __fdividef(0.999999f, f.hi - f.lo) : 1e-37f;
   return f;
 }
 

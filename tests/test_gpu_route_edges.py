@@ -57,3 +57,26 @@ def test_infinite_logits_tie_with_the_largest(moe, e, groups):
     x[:, e - 1] = INF
     for score in ("softmax", "sigmoid"):
         check(moe, x, None, 2, score, groups, 1, "max", grad=False)
+
+
+# ---- keys beyond the fixed-point range in every lane
+
+@pytest.mark.parametrize("e", [128, 256, 1000])
+def test_a_largest_key_in_every_lane(moe, e):
+    x = draw(24, 6, e, False)
+    inf = x.clone()
+    inf[:, 1::4] = INF
+    check(moe, inf, None, 5, "sigmoid", grad=False)
+    inf[:, 2::4] = MOST
+    check(moe, inf, None, 5, "sigmoid", grad=False)
+    bias = draw_bias(24, e)
+    bias[1::4] = INF
+    for score in ("softmax", "sigmoid"):
+        check(moe, x, bias, 5, score, grad=False)
+    # all but a few
+    few = torch.full_like(x, INF)
+    few[:, 3:80:4] = x[:, 3:80:4]
+    check(moe, few, None, 5, "sigmoid", grad=False)
+    bias.fill_(INF)
+    bias[3:80:4] = 0.1
+    check(moe, x, bias, 5, "softmax", grad=False)

@@ -10,7 +10,8 @@
 // heads, and the lane that gave it reads its next.
 //
 // Fixed point covers the keys from the smallest lane maximum up (32 lanes hold
-// 32 keys at least that large, and k <= 32), which is about as fine as fp32.
+// 32 keys at least that large, and k <= 32), and below it those that lie within
+// the keys' errors, which is about as fine as fp32.
 // It is monotone, so keys that differ in it are in order; where two keys whose
 // order matters do not differ by more than the keys' own errors, the experts
 // in question get fp64 keys (settle_groups, settle_order; where they are more
@@ -341,7 +342,7 @@ __device__ __forceinline__ void sort_down(unsigned (&v)[V]) {
 // Keys in [lo, lo + range] as 1 .. 2^22 - 1, monotone; smaller keys, and those
 // of experts that are taken out (-inf, NaN), are 0.
 struct FixedPoint {
-  float lo, hi, per_range;
+  float lo, hi, per_range, margin;
   __device__ __forceinline__ unsigned bits(float key) const {
     // the saturating sum ends at 0 and 1 and takes NaN to 0; 2^23 puts the
     // steps into the low bits
@@ -355,8 +356,10 @@ struct FixedPoint {
 
 constexpr float kOrdinary = 1e30f;  // larger magnitudes (masks of the type's lowest value) share the ends of the range
 
+// exact: keys are what they stand for; else err is how far one may be off beside
+// its own rounding.
 template <int V>
-__device__ __forceinline__ FixedPoint range_of(const float (&key)[V]) {
+__device__ __forceinline__ FixedPoint range_of(const float (&key)[V], bool exact, float err) {
   float most = -INFINITY;
 #pragma unroll
   for (int i = 0; i < V; ++i) most = fmaxf(most, key[i]);
@@ -371,6 +374,12 @@ __device__ __forceinline__ FixedPoint range_of(const float (&key)[V]) {
       if (key[i] >= -kOrdinary) least = fminf(least, key[i]);
   }
   f.lo = fminf(unordered(__reduce_min_sync(kAll, ordered(least))), f.hi);
+  // Two keys whose order is open are at most margin apart. One that could
+  // belong before the smallest lane maximum has to be in the range too: where
+  // the k = 32 places are the lanes' maxima, only then does it show behind the
+  // last. (Twice, for the difference's own rounding.)
+  f.margin = exact ? 0.0f : 2.0f * (err + kUnit * fmaxf(fabsf(f.lo), fabsf(f.hi)));
+  f.lo -= 2.0f * f.margin;
   // (Without a range keys from lo up are one step; not times 0, which would
   // lose those that are infinite.)
   f.per_range = f.hi > f.lo ? __fdividef(0.999999f, f.hi - f.lo) : 1e-37f;
@@ -567,7 +576,8 @@ __global__ void __launch_bounds__(kRouteWarps * 32, V <= 8 ? 8 : V <= 16 ? 6 : 4
     }
   }
 
-  const FixedPoint fixed = range_of<V>(key);
+  const bool exact = !(SCORED && p.bias);  // without a bias the keys are logits by now
+  const FixedPoint fixed = range_of<V>(key, exact, err);
   unsigned head;       // the largest of this lane's list
   unsigned own = 0;    // what place `lane` got
   {
@@ -607,8 +617,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32, V <= 8 ? 8 : V <= 16 ? 6 : 4
     // for logits, which only have to differ. Equal logits with equal biases
     // are equal in any arithmetic.
     unsigned slack = 0;
-    if (SCORED && p.bias)
-      slack = (unsigned)fminf(2.0f * (err + kUnit * fmaxf(fabsf(fixed.lo), fabsf(fixed.hi))) * fixed.per_range * 4194304.0f, 4e6f) + 3u;
+    if (!exact) slack = (unsigned)fminf(fixed.margin * fixed.per_range * 4194304.0f, 4e6f) + 3u;
     const unsigned after = __shfl_down_sync(kAll, own, 1), next = __reduce_max_sync(kAll, head);
     const unsigned below = lane == p.topk - 1 ? next : after;
     bool near = own && below >= 1024 && (own >> 10) - (below >> 10) <= slack;

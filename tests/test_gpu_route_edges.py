@@ -80,3 +80,32 @@ def test_a_largest_key_in_every_lane(moe, e):
     bias.fill_(INF)
     bias[3:80:4] = 0.1
     check(moe, x, bias, 5, "softmax", grad=False)
+
+
+# ---- what lies behind the last place
+
+def from_keys(key, bias):
+    """Logits (fp32) whose sigmoid + bias is about key (float64 [N, E])."""
+    s = key - bias.astype(np.float64)
+    x = torch.tensor(np.log(s / (1 - s)), dtype=torch.float32, device=DEV)
+    return x, torch.from_numpy(bias).to(DEV)
+
+
+@pytest.mark.parametrize("e", [128, 256, 1024])
+def test_the_thirty_third_key_behind_thirty_two_lanes(moe, e):
+    # the 32 largest keys lie one to a lane (experts 4 l), and the next one is
+    # within an fp32 step or so of the smallest of them
+    g, n = np.random.default_rng(25), 300
+    bias = (0.02 * g.standard_normal(e)).astype(np.float32)
+    key = 0.6 + 0.01 * g.random((n, e))
+    tops = 0.75 + 1e-3 * g.random((n, 32))
+    key[:, 0:128:4] = tops
+    rows = np.arange(n)
+    low = 4 * tops.argmin(1)
+    rival = (4 * g.integers(0, 32, n) + 1)
+    key[rows, rival] = key[rows, low] + g.uniform(-1, 1, n) * 2.0 ** -25
+    x, b = from_keys(key, bias)
+    true = 1 / (1 + np.exp(-x.double().cpu().numpy())) + bias.astype(np.float64)
+    gap = true[rows, rival] - true[rows, low]
+    assert 0.2 < (gap > 0).mean() < 0.8 and (np.abs(gap) > 1e-14).all()  # decided either way, and defined
+    check(moe, x, b, 32, "sigmoid", grad=False)

@@ -615,7 +615,8 @@ __global__ void __launch_bounds__(kRouteWarps * 32, V <= 8 ? 8 : V <= 16 ? 6 : 4
     // An order is open where a place and the next (behind the last place: the
     // largest that is left) lie within the keys' error of one another: none
     // for logits, which only have to differ. Equal logits with equal biases
-    // are equal in any arithmetic.
+    // are equal in any arithmetic; but behind the last place such a one may
+    // stand before others that are larger in 64 bits.
     unsigned slack = 0;
     if (!exact) slack = (unsigned)fminf(fixed.margin * fixed.per_range * 4194304.0f, 4e6f) + 3u;
     const unsigned after = __shfl_down_sync(kAll, own, 1), next = __reduce_max_sync(kAll, head);
@@ -623,22 +624,39 @@ __global__ void __launch_bounds__(kRouteWarps * 32, V <= 8 ? 8 : V <= 16 ? 6 : 4
     bool near = own && below >= 1024 && (own >> 10) - (below >> 10) <= slack;
     if (__any_sync(kAll, near)) {
       const int other = 1023 - (int)(below & 1023u);
-      if (near && load_logit(p, t, mine) == load_logit(p, t, other) &&
-          (!p.bias || p.bias[mine] == p.bias[other]))
-        near = false;
-      if (__any_sync(kAll, near) && !open) {
-        const unsigned last = __reduce_min_sync(kAll, own ? own >> 10 : 0xffffffffu);
-        unsigned mask = 0;
+      const bool same = near && load_logit(p, t, mine) == load_logit(p, t, other) &&
+                        (!p.bias || p.bias[mine] == p.bias[other]);
+      near = near && !same;
+      const bool tied = __any_sync(kAll, same && lane == p.topk - 1);
+      if ((tied || __any_sync(kAll, near)) && !open) {
+        // the experts in question, and of those that are not chosen the ones
+        // that may differ from the last (exact keys are the logits)
+        const unsigned end = __reduce_min_sync(kAll, own ? own : 0xffffffffu);
+        const int e_end = 1023 - (int)(end & 1023u);
+        const float x_end = load_logit(p, t, e_end);
+        unsigned mask = 0, left = 0;
 #pragma unroll
-        for (int i = 0; i < V; ++i)
-          if (key[i] > -INFINITY && fixed.of(key[i]) + slack >= last) mask |= 1u << i;
-        int total;
-        int* seats = reinterpret_cast<int*>(room);
-        const int e = share_out(mask, seats, total);
-        if (total <= 32)
-          mine = settle_order(p, t, e, total, top, seats);
-        else
-          open = true;
+        for (int i = 0; i < V; ++i) {
+          const unsigned v = fixed.packed(key[i], (i / 4) * 128 + lane * 4 + i % 4);
+          if (key[i] > -INFINITY && (v >> 10) + slack >= end >> 10) {
+            mask |= 1u << i;
+            if (v < end && !(exact && key[i] == x_end)) left |= 1u << i;
+          }
+        }
+        if (tied)
+          for (; left && !near; left &= left - 1) {
+            const int i = __ffs(left) - 1, e = (i / 4) * 128 + lane * 4 + i % 4;
+            near = load_logit(p, t, e) != x_end || (p.bias && p.bias[e] != p.bias[e_end]);
+          }
+        if (__any_sync(kAll, near)) {
+          int total;
+          int* seats = reinterpret_cast<int*>(room);
+          const int e = share_out(mask, seats, total);
+          if (total <= 32)
+            mine = settle_order(p, t, e, total, top, seats);
+          else
+            open = true;
+        }
       }
     }
     if (open) mine = order_in_64(p, t, room, top);

@@ -109,3 +109,55 @@ def test_the_thirty_third_key_behind_thirty_two_lanes(moe, e):
     gap = true[rows, rival] - true[rows, low]
     assert 0.2 < (gap > 0).mean() < 0.8 and (np.abs(gap) > 1e-14).all()  # decided either way, and defined
     check(moe, x, b, 32, "sigmoid", grad=False)
+
+
+@pytest.mark.parametrize("groups", [1, 4])
+@pytest.mark.parametrize("k", [1, 3])
+def test_a_larger_key_behind_an_equal_one(moe, k, groups):
+    # two equal keys, one of them at the last place, and a third that is larger
+    # only in 64 bits
+    e = 128
+    for bf16 in (False, True):
+        x = draw(26, 40, e, bf16).clamp(-4, 4)
+        for r in range(40):
+            at = [2 + r % 20, 23 + r % 5, 90 + r % 20]
+            x[r, 100:100 + k - 1] = 30.0 + r % 2
+            x[r, at[:2]] = 20.0
+            x[r, at[2]] = 21.0
+            if k > 1:
+                x[r, 120:120 + k - 1] = 9.0  # in the way of nothing
+        for b in (torch.zeros(e, device=DEV), torch.full((e,), 0.25, device=DEV)):
+            check(moe, x, b, k, "sigmoid", groups, groups, "max", grad=False)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_a_larger_logit_behind_an_equal_one_in_one_step(moe, score):
+    # an outlier stretches the range, so that 0.5 and 0.50001 are one step
+    x = torch.zeros(3, 256, device=DEV)
+    x[:, 200] = 1000.0
+    x[:, [10, 11]] = 0.5
+    x[:, 30] = 0.50001
+    x[1, 31] = 0.50002
+    x[2, 9] = 0.49999
+    for k in (2, 3):
+        check(moe, x, None, k, score, grad=False)
+
+
+def test_equal_keys_in_plenty(moe):
+    # ties alone stay with the lower index, however many there are
+    for bf16 in (False, True):
+        x = (draw(27, 60, 256, bf16) * 2).round() / 2
+        for b in (None, torch.zeros(256, device=DEV)):
+            check(moe, x, b, 8, "sigmoid", grad=False)
+            check(moe, x, b, 32, "softmax", grad=False)
+            check(moe, x, b, 8, "sigmoid", 8, 4, "top2", grad=False)
+
+
+def test_masks_of_large_finite_values(moe):
+    for mask in (-1e4, -1e9, -1e30, -3e38):
+        for e in (128, 256):
+            x = draw(28, 20, e, False)
+            x[:, 4:8] = mask
+            x[3:, 64:] = mask
+            check(moe, x, None, 6, "softmax", grad=False)
+            check(moe, x, draw_bias(28, e), 6, "softmax", 8, 4, "top2", grad=False)

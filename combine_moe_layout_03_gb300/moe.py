@@ -1097,10 +1097,13 @@ def prepare_expert_product_backward_weight(desc: MoeExpertDesc, grad_y, x, row_b
 
 def moe_expert_product_backward_weight(desc: MoeExpertDesc, grad_y, x, row_begin, row_end, grad_w=None,
                                        grad_kind: int = MOE_GRAD_BF16, stream=None):
-    """grad_w[e] = sum of grad_y[s]^T x[s] over e's rows, written as bf16 or fp32 or added to an fp32 grad_w.
-    Returns grad_w [E, N, K]."""
+    """grad_w[e] = sum of grad_y[s]^T x[s] over e's rows, written as bf16 or fp32 or added to an fp32 grad_w (written
+    where none is given). Returns grad_w [E, N, K]."""
     if grad_w is None:
-        grad_w = torch.zeros((desc.num_experts, desc.out_features, desc.in_features), device=row_begin.device,
+        # every element is written, those of experts without rows too
+        if grad_kind == MOE_GRAD_F32_ADD:
+            grad_kind = MOE_GRAD_F32
+        grad_w = torch.empty((desc.num_experts, desc.out_features, desc.in_features), device=row_begin.device,
                              dtype=torch.bfloat16 if grad_kind == MOE_GRAD_BF16 else torch.float32)
     prepare_expert_product_backward_weight(desc, grad_y, x, row_begin, row_end, grad_w, grad_kind, stream)()
     return grad_w

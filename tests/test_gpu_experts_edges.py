@@ -87,3 +87,21 @@ def test_a_long_reduction_outlasts_the_budget_of_a_wait(moe):
     finally:
         moe.moe_set_wait_limit_ns(0)
     assert torch.equal(dw, want)
+
+
+def test_a_weight_gradient_without_a_buffer(moe):
+    # experts without rows get zeros whatever the memory held; added to nothing is written
+    counts = [37, 0, 130, 0]
+    begin, end = ranges(counts, DEV)
+    x, dy = whole(1, 167, 72), whole(2, 167, 136)
+    d = moe.MoeExpertDesc(4, 167, 72, 136)
+    want = sums(dy, x, begin, end)
+    for kind, t in ((moe.MOE_GRAD_BF16, torch.bfloat16), (moe.MOE_GRAD_F32, torch.float32), (moe.MOE_GRAD_F32_ADD, torch.float32)):
+        for _ in range(3):
+            junk = torch.full((4, 136, 72), float("nan"), dtype=t, device=DEV)
+            del junk
+            dw = moe.moe_expert_product_backward_weight(d, dy, x, begin, end, grad_kind=kind)
+            assert torch.equal(dw, want.to(t))
+    none = moe.MoeExpertDesc(4, 0, 72, 136)
+    dw = moe.moe_expert_product_backward_weight(none, None, None, begin, end, grad_kind=moe.MOE_GRAD_F32_ADD)
+    assert bool((dw == 0).all())

@@ -873,6 +873,18 @@ class MoeExpertDesc:
         return _ExpertDesc(self.rows, self.x_stride, self.num_experts, self.in_features, self.out_features)
 
 
+def _fresh(shape, dtype, device, stream):
+    """An output of a call on `stream`, out of that stream's memory: a block of the current stream's may still be
+    written by what is queued there."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = _stream(stream)
+        stream = torch.cuda.ExternalStream(handle, device=device) if handle else torch.cuda.default_stream(device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _want(what: str, t, dtype, numel: int, optional: bool = False):
     """t is a dense CUDA tensor of dtype with at least numel elements."""
     if t is None:
@@ -932,9 +944,9 @@ def moe_route(desc: MoeRouteDesc, logits, bias=None, topk_idx=None, topk_weights
     Returns (topk_idx int32 [N, k], topk_weights fp32 [N, k])."""
     shape = (desc.num_tokens, desc.topk)
     if topk_idx is None:
-        topk_idx = torch.empty(shape, dtype=torch.int32, device=logits.device)
+        topk_idx = _fresh(shape, torch.int32, logits.device, stream)
     if topk_weights is None:
-        topk_weights = torch.empty(shape, dtype=torch.float32, device=logits.device)
+        topk_weights = _fresh(shape, torch.float32, logits.device, stream)
     prepare_route(desc, logits, bias, topk_idx, topk_weights, stream)()
     return topk_idx, topk_weights
 
@@ -953,7 +965,7 @@ def prepare_route_backward(desc: MoeRouteDesc, logits, topk_idx, grad_weights, g
 def moe_route_backward(desc: MoeRouteDesc, logits, topk_idx, grad_weights, grad_logits=None, stream=None):
     """Gradient of the logits, [N, E] of their type (see include/moe.h)."""
     if grad_logits is None:
-        grad_logits = torch.empty((desc.num_tokens, desc.num_experts), dtype=desc.logits_dtype, device=logits.device)
+        grad_logits = _fresh((desc.num_tokens, desc.num_experts), desc.logits_dtype, logits.device, stream)
     prepare_route_backward(desc, logits, topk_idx, grad_weights, grad_logits, stream)()
     return grad_logits
 
@@ -982,7 +994,7 @@ def prepare_swiglu(desc: MoeGluDesc, gate_up, act, ckpt=None, ckpt_scales=None, 
 def moe_swiglu(desc: MoeGluDesc, gate_up, act=None, ckpt=None, ckpt_scales=None, num_rows=None, stream=None):
     """act = silu(gate) * up, and the checkpoint if buffers for it are given. Returns act bf16 [rows, F]."""
     if act is None:
-        act = torch.empty((desc.rows, desc.width), dtype=torch.bfloat16, device=gate_up.device)
+        act = _fresh((desc.rows, desc.width), torch.bfloat16, gate_up.device, stream)
     prepare_swiglu(desc, gate_up, act, ckpt, ckpt_scales, num_rows, stream)()
     return act
 
@@ -1005,7 +1017,7 @@ def moe_swiglu_backward(desc: MoeGluDesc, ckpt, ckpt_scales, grad_act, grad_gate
     """Gradient of gate|up from the checkpoint; act (if given) receives the activation again.
     Returns grad_gate_up bf16 [rows, 2F]."""
     if grad_gate_up is None:
-        grad_gate_up = torch.empty((desc.rows, 2 * desc.width), dtype=torch.bfloat16, device=grad_act.device)
+        grad_gate_up = _fresh((desc.rows, 2 * desc.width), torch.bfloat16, grad_act.device, stream)
     prepare_swiglu_backward(desc, ckpt, ckpt_scales, grad_act, grad_gate_up, act, num_rows, stream)()
     return grad_gate_up
 
@@ -1035,7 +1047,7 @@ def prepare_expert_product(desc: MoeExpertDesc, x, row_begin, row_end, w, y, str
 def moe_expert_product(desc: MoeExpertDesc, x, row_begin, row_end, w, y=None, stream=None):
     """y[s] = w[e] x[s] for the rows of every expert (see include/moe.h). Returns y bf16 [rows, N]."""
     if y is None:
-        y = torch.empty((desc.rows, desc.out_features), dtype=torch.bfloat16, device=w.device)
+        y = _fresh((desc.rows, desc.out_features), torch.bfloat16, w.device, stream)
     prepare_expert_product(desc, x, row_begin, row_end, w, y, stream)()
     return y
 
@@ -1057,7 +1069,7 @@ def moe_expert_swiglu(desc: MoeExpertDesc, x, row_begin, row_end, w, act=None, c
     """silu(gate) * up with gate|up = w[e] x[s], w [E, 2F, K], desc.out_features = F; and the checkpoint if buffers
     for it are given (swiglu_checkpoint). Returns act bf16 [rows, F]."""
     if act is None:
-        act = torch.empty((desc.rows, desc.out_features), dtype=torch.bfloat16, device=w.device)
+        act = _fresh((desc.rows, desc.out_features), torch.bfloat16, w.device, stream)
     prepare_expert_swiglu(desc, x, row_begin, row_end, w, act, ckpt, ckpt_scales, stream)()
     return act
 
@@ -1077,7 +1089,7 @@ def prepare_expert_product_backward_input(desc: MoeExpertDesc, grad_y, row_begin
 def moe_expert_product_backward_input(desc: MoeExpertDesc, grad_y, row_begin, row_end, w, grad_x=None, stream=None):
     """grad_x[s] = w[e]^T grad_y[s]. Returns grad_x bf16 [rows, K]."""
     if grad_x is None:
-        grad_x = torch.empty((desc.rows, desc.in_features), dtype=torch.bfloat16, device=w.device)
+        grad_x = _fresh((desc.rows, desc.in_features), torch.bfloat16, w.device, stream)
     prepare_expert_product_backward_input(desc, grad_y, row_begin, row_end, w, grad_x, stream)()
     return grad_x
 
@@ -1103,8 +1115,8 @@ def moe_expert_product_backward_weight(desc: MoeExpertDesc, grad_y, x, row_begin
         # every element is written, those of experts without rows too
         if grad_kind == MOE_GRAD_F32_ADD:
             grad_kind = MOE_GRAD_F32
-        grad_w = torch.empty((desc.num_experts, desc.out_features, desc.in_features), device=row_begin.device,
-                             dtype=torch.bfloat16 if grad_kind == MOE_GRAD_BF16 else torch.float32)
+        grad_w = _fresh((desc.num_experts, desc.out_features, desc.in_features),
+                        torch.bfloat16 if grad_kind == MOE_GRAD_BF16 else torch.float32, row_begin.device, stream)
     prepare_expert_product_backward_weight(desc, grad_y, x, row_begin, row_end, grad_w, grad_kind, stream)()
     return grad_w
 

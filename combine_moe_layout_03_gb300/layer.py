@@ -45,9 +45,16 @@ class MoeLayer:
         pairs = moe.MoeDesc(n, self.topk, self.num_experts, self.num_ranks, self.hidden)
         return route, pairs
 
+    def _want_tokens(self, what: str, t, n: int):
+        """Dispatch and combine see pointers only: rows have to lie one behind the other."""
+        if t.dim() != 2 or t.shape[0] != n or t.shape[1] != self.hidden:
+            raise moe.MoeError(moe.MOE_ERR_SHAPE, f"{what}: [{n}, {self.hidden}] is wanted, not {list(t.shape)}")
+        moe._want(what, t, torch.bfloat16, n * self.hidden)
+
     def forward(self, x, logits, w1, w2, bias=None, train: bool = False):
-        """x bf16 [N, H], logits fp32 or bf16 [N, E] -> (out bf16 [N, H], what backward needs or None)."""
+        """x bf16 [N, H] (dense), logits fp32 or bf16 [N, E] -> (out bf16 [N, H], what backward needs or None)."""
         n, h, f = x.shape[0], self.hidden, self.width
+        self._want_tokens("x", x, n)
         route, d = self._descs(n, logits)
         idx, weights = moe.moe_route(route, logits, bias)
         lay, rec = moe.moe_layout_dispatch(d, idx, weights, x, None)
@@ -65,8 +72,9 @@ class MoeLayer:
 
     def backward(self, kept: dict, grad_out, w1, w2, grad_kind: int = moe.MOE_GRAD_F32, grad_w1=None, grad_w2=None) -> dict:
         """Gradients of x (bf16), logits (their type), w1 and w2 (grad_kind; written or, with MOE_GRAD_F32_ADD, added
-        to grad_w1 and grad_w2)."""
+        to grad_w1 and grad_w2). grad_out is bf16 [N, H], dense."""
         d, lay, rows = kept["d"], kept["lay"], kept["rows"]
+        self._want_tokens("grad_out", grad_out, d.num_tokens)
         h, f, p = self.hidden, self.width, d.num_tokens * self.topk
         begin, end = moe.expert_row_ranges(lay)
         used = lay["expert_offset"][-1:]  # rows that hold a pair

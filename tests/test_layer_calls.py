@@ -34,3 +34,43 @@ def test_a_weight_gradient_without_a_buffer_is_not_filled_first(moe, monkeypatch
         mine = torch.empty(3, 8, 16)
         assert moe.moe_expert_product_backward_weight(moe.MoeExpertDesc(3, 5, 16, 8), None, None, ids, ids, mine, kind) is mine
         assert seen[-1][0] is mine and seen[-1][1] == kind
+
+
+class OnGpu(torch.Tensor):
+    """A host tensor that passes for one on the GPU (nothing is launched)."""
+    is_cuda = property(lambda self: True)
+
+
+def test_the_layer_refuses_tokens_that_are_not_dense_rows(moe, monkeypatch):
+    # dispatch, combine and their backward take pointers: an expanded gradient
+    # (of a sum) would be read behind its one element
+    from combine_moe_layout_03_gb300.layer import MoeLayer
+
+    def launched(*args, **kw):
+        raise AssertionError("launched")
+
+    for name in ("moe_route", "moe_layout_dispatch", "moe_combine_backward"):
+        monkeypatch.setattr(moe, name, launched)
+    n, h = 6, 16
+    layer = MoeLayer(h, 8, 4, 2)
+    kept = dict(d=moe.MoeDesc(n, 2, 4, 1, h), lay=dict(expert_offset=torch.zeros(5, dtype=torch.int32), slot_of=None), rows=None, weights=None, y=None)
+    bf16 = lambda t: t.bfloat16().as_subclass(OnGpu)  # noqa: E731
+    wide = bf16(torch.zeros(n, 2 * h))
+    bad = [bf16(torch.ones(())).expand(n, h), bf16(torch.zeros(h)).expand(n, h), wide[:, :h], bf16(torch.zeros(h, n)).t(),
+           torch.zeros(n, h).as_subclass(OnGpu), torch.zeros(n, h).bfloat16()]
+    for t in bad:
+        for call in (lambda: layer.forward(t, torch.zeros(n, 4), None, None), lambda: layer.backward(kept, t, None, None)):
+            with pytest.raises(moe.MoeError) as err:
+                call()
+            assert err.value.code == moe.MOE_ERR_INVALID_ARG
+    for t in (wide, bf16(torch.zeros(n * h))):
+        with pytest.raises(moe.MoeError) as err:
+            layer.forward(t, torch.zeros(n, 4), None, None)
+        assert err.value.code == moe.MOE_ERR_SHAPE
+    with pytest.raises(moe.MoeError) as err:
+        layer.backward(kept, bf16(torch.zeros(n - 1, h)), None, None)
+    assert err.value.code == moe.MOE_ERR_SHAPE
+    good = bf16(torch.zeros(n, h))
+    for call in (lambda: layer.forward(good, torch.zeros(n, 4), None, None), lambda: layer.backward(kept, good, None, None)):
+        with pytest.raises(AssertionError, match="launched"):
+            call()

@@ -897,35 +897,37 @@ def _want(what: str, t, dtype, numel: int, optional: bool = False):
         raise MoeError(MOE_ERR_CAPACITY, f"{what}: {t.numel()} elements, {numel} needed")
 
 
-def _want_rows(what: str, t, rows: int, width: int, stride: int):
-    """t is a bf16 CUDA tensor holding `rows` rows of `width` elements, `stride` apart."""
+def _want_rows(what: str, t, dtype, rows: int, width: int, stride: int):
+    """t is a CUDA tensor of dtype that holds `rows` rows of `width` elements, `stride` apart; dimensions before the
+    last count as rows if they lie evenly."""
     if t is None:
         if rows <= 0:
             return
         raise MoeError(MOE_ERR_INVALID_ARG, f"{what}: missing")
-    if t.dtype != torch.bfloat16 or not t.is_cuda or (t.dim() and t.numel() and t.stride(-1) != 1):
-        raise MoeError(MOE_ERR_INVALID_ARG, f"{what}: a bf16 CUDA tensor with dense rows is wanted")
-    have = t.untyped_storage().nbytes() // 2 - t.storage_offset()
-    if rows > 0 and have < (rows - 1) * stride + width:
+    if t.dtype != dtype or not t.is_cuda:
+        raise MoeError(MOE_ERR_INVALID_ARG, f"{what}: a CUDA tensor of {dtype} is wanted")
+    if rows <= 0:
+        return
+    if t.numel() == 0:
+        raise MoeError(MOE_ERR_CAPACITY, f"{what}: empty, {rows} rows of {width} needed")
+    dims = [(n, d) for n, d in zip(t.shape, t.stride()) if n > 1]
+    block = 1  # a dense run of elements, as many dimensions from the last as make a row
+    while dims and block < width and dims[-1][1] == block:
+        block *= dims.pop()[0]
+    have, apart = block, stride
+    for n, d in reversed(dims):
+        if d != apart or block < width:
+            raise MoeError(MOE_ERR_INVALID_ARG,
+                           f"{what}: dense rows of {width}, {stride} apart, are wanted, not {list(t.shape)} with strides {list(t.stride())}")
+        have += (n - 1) * d
+        apart *= n
+    if have < (rows - 1) * stride + width:
         raise MoeError(MOE_ERR_CAPACITY, f"{what}: {have} elements, {(rows - 1) * stride + width} needed")
-    if t.dim() == 2 and t.shape[0] > 1 and t.stride(0) != stride:
-        raise MoeError(MOE_ERR_INVALID_ARG, f"{what}: rows are {t.stride(0)} elements apart, the descriptor says {stride}")
 
 
 def _want_logits(desc: MoeRouteDesc, logits):
-    n, e = desc.num_tokens, desc.num_experts
-    stride = desc.logits_stride or e
-    if logits is None:
-        _want("logits", None, desc.logits_dtype, n * e)
-        return
-    if logits.dtype != desc.logits_dtype or not logits.is_cuda or (logits.numel() and logits.stride(-1) != 1):
-        raise MoeError(MOE_ERR_INVALID_ARG, f"logits: a CUDA tensor of {desc.logits_dtype} with dense rows is wanted")
-    have = logits.untyped_storage().nbytes() // logits.element_size() - logits.storage_offset()
-    if n > 0 and have < (n - 1) * stride + e:
-        raise MoeError(MOE_ERR_CAPACITY, f"logits: {have} elements, {(n - 1) * stride + e} needed")
-    if logits.dim() == 2 and logits.shape[0] > 1 and logits.stride(0) != stride:
-        raise MoeError(MOE_ERR_INVALID_ARG,
-                       f"logits: rows are {logits.stride(0)} elements apart, the descriptor says {stride}")
+    _want_rows("logits", logits, desc.logits_dtype, desc.num_tokens, desc.num_experts,
+               desc.logits_stride or desc.num_experts)
 
 
 def prepare_route(desc: MoeRouteDesc, logits, bias, topk_idx, topk_weights, stream=None) -> Prepared:
@@ -1036,7 +1038,7 @@ def _want_experts(desc: MoeExpertDesc, row_begin, row_end):
 def prepare_expert_product(desc: MoeExpertDesc, x, row_begin, row_end, w, y, stream=None) -> Prepared:
     e, r, k, n = desc.num_experts, desc.rows, desc.in_features, desc.out_features
     _want_experts(desc, row_begin, row_end)
-    _want_rows("x", x, r, k, desc.x_stride or k)
+    _want_rows("x", x, torch.bfloat16, r, k, desc.x_stride or k)
     _want("w", w, torch.bfloat16, e * n * k)
     _want("y", y, torch.bfloat16, r * n)
     d = desc.c()
@@ -1056,7 +1058,7 @@ def prepare_expert_swiglu(desc: MoeExpertDesc, x, row_begin, row_end, w, act, ck
                           stream=None) -> Prepared:
     e, r, k, f = desc.num_experts, desc.rows, desc.in_features, desc.out_features
     _want_experts(desc, row_begin, row_end)
-    _want_rows("x", x, r, k, desc.x_stride or k)
+    _want_rows("x", x, torch.bfloat16, r, k, desc.x_stride or k)
     _want("w", w, torch.bfloat16, e * 2 * f * k)
     _want("act", act, torch.bfloat16, r * f)
     _want_checkpoint(MoeGluDesc(r, f), ckpt, ckpt_scales, optional=True)
@@ -1099,7 +1101,7 @@ def prepare_expert_product_backward_weight(desc: MoeExpertDesc, grad_y, x, row_b
     e, r, k, n = desc.num_experts, desc.rows, desc.in_features, desc.out_features
     _want_experts(desc, row_begin, row_end)
     _want("grad_y", grad_y, torch.bfloat16, r * n)
-    _want_rows("x", x, r, k, desc.x_stride or k)
+    _want_rows("x", x, torch.bfloat16, r, k, desc.x_stride or k)
     _want("grad_w", grad_w, torch.bfloat16 if grad_kind == MOE_GRAD_BF16 else torch.float32, e * n * k)
     d = desc.c()
     args = (ctypes.byref(d), *_vps(grad_y, x, row_begin, row_end, grad_w), ctypes.c_int(grad_kind),

@@ -74,3 +74,41 @@ def test_the_layer_refuses_tokens_that_are_not_dense_rows(moe, monkeypatch):
     for call in (lambda: layer.forward(good, torch.zeros(n, 4), None, None), lambda: layer.backward(kept, good, None, None)):
         with pytest.raises(AssertionError, match="launched"):
             call()
+
+
+def test_rows_that_lie_as_the_descriptor_says(moe):
+    t = torch.zeros(4, 3, 24)
+    on = lambda v: v.as_subclass(OnGpu)  # noqa: E731
+    want = lambda v, rows, width, stride: moe._want_rows("x", on(v), torch.float32, rows, width, stride)  # noqa: E731
+    # dense, whatever the shape; padded rows; a batch of padded rows; one row; a column of width 1
+    for args in ((t, 12, 24, 24), (t.view(12, 24), 12, 24, 24), (t.view(-1), 12, 24, 24), (t.view(24, 12), 12, 24, 24),
+                 (t.view(12, 2, 12), 12, 24, 24), (t.view(1, 12, 24), 5, 24, 24),
+                 (t.view(12, 24)[:, 8:], 12, 16, 24), (t[..., 8:], 12, 16, 24), (t[:, :, :16], 11, 16, 24), (t, 12, 16, 24),
+                 (t.view(12, 24)[5:6, :8], 1, 8, 8), (t.view(12, 24)[::2], 6, 24, 48), (t.view(12, 24)[:, 7:8], 12, 1, 24),
+                 (t.view(1, 288).t(), 288, 1, 1), (torch.zeros(0, 24), 0, 24, 24)):
+        want(*args)
+    # rows further apart than the descriptor says, uneven ones, columns, repeated rows
+    for args in ((t[..., 8:], 12, 16, 16), (t[..., :16], 12, 16, 16), (t[:, :2], 8, 24, 24), (t[:, ::2, 8:], 8, 16, 24),
+                 (t.transpose(0, 1), 12, 24, 24), (t.view(12, 24).t(), 24, 12, 12), (torch.zeros(24).expand(12, 24), 12, 24, 24),
+                 (t.view(12, 24)[:, ::2], 12, 12, 24), (t.view(4, 72), 12, 24, 24), (t.view(12, 24), 12, 16, 16), (t.view(12, 24)[:, 8:], 12, 16, 16),
+                 (torch.zeros(()).expand(12, 1), 12, 1, 1)):
+        with pytest.raises(moe.MoeError) as err:
+            want(*args)
+        assert err.value.code == moe.MOE_ERR_INVALID_ARG, args[1:]
+    # too few rows in the view, whatever its storage holds
+    for args in ((t.view(12, 24)[:5], 6, 24, 24), (t[..., 8:], 13, 16, 24), (t.view(-1)[:280], 12, 24, 24), (torch.zeros(0, 24), 1, 24, 24)):
+        with pytest.raises(moe.MoeError) as err:
+            want(*args)
+        assert err.value.code == moe.MOE_ERR_CAPACITY, args[1:]
+    # through the calls: a batch of padded rows needs its stride named
+    x = on(torch.zeros(2, 3, 72, dtype=torch.bfloat16))[..., 8:]
+    ids = on(torch.zeros(2, dtype=torch.int32))
+    w, y = on(torch.zeros(2, 8, 64, dtype=torch.bfloat16)), on(torch.zeros(6, 8, dtype=torch.bfloat16))
+    with pytest.raises(moe.MoeError):
+        moe.prepare_expert_product(moe.MoeExpertDesc(2, 6, 64, 8), x, ids, ids, w, y, stream=0)
+    moe.prepare_expert_product(moe.MoeExpertDesc(2, 6, 64, 8, x_stride=72), x, ids, ids, w, y, stream=0)
+    logits = on(torch.zeros(2, 3, 20))[..., :16]
+    out, weights = on(torch.zeros(6, 2, dtype=torch.int32)), on(torch.zeros(6, 2))
+    with pytest.raises(moe.MoeError):
+        moe.prepare_route(moe.MoeRouteDesc(6, 16, 2), logits, None, out, weights, stream=0)
+    moe.prepare_route(moe.MoeRouteDesc(6, 16, 2, logits_stride=20), logits, None, out, weights, stream=0)

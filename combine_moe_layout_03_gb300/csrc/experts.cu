@@ -33,14 +33,14 @@
 // sustained under the power cap). Many rows: the tensor cores, a step of a
 // 256 x 256 tile takes 515 cycles of which 512 are theirs, and then the power
 // cap: 16384 rows x 7168 -> 4096 over 32 experts of 512 take 522 us (1840
-// TFLOP/s) in short runs and 573 to 618 us (a library's batched product 614 us)
+// TFLOP/s) in short runs and 573 to 643 us (a library's batched product 614 us)
 // in long ones. A tile of n rows takes 2 n cycles a step in the tensor cores,
 // and 256 + n for its operands (16 KB of features and 64 n bytes of rows for
 // each SM, at 64 bytes a cycle from L2; measured 452 cycles at 192 rows, 504 at
 // 224): 480 rows an expert 501 to 538 us, 416 rows 492; experts of 412 to 616
-// rows take 670 us in long runs. Few rows: the weights, 8 rows an expert 274
-// us for 1.88 GB (6.9 TB/s). Weight gradients: their result, 3.76 GB of fp32
-// 780 us.
+// rows take 670 to 725 us in long runs. Few rows: the weights, 8 rows an expert
+// 274 to 283 us for 1.88 GB (6.9 TB/s). Weight gradients: their result, 3.76 GB
+// of fp32 780 to 880 us (bf16 695 to 705, added to fp32 1483).
 #include <cuda.h>
 
 #include <mutex>

@@ -18,6 +18,13 @@
 // than 32, order_in_64 does the whole token), so that the choice is always
 // that of 64-bit arithmetic. For 256 experts with a bias that happens to about
 // one token in five hundred, and costs it two microseconds.
+//
+// The range is only as fine as it is short. A lane whose largest key is a mask
+// of -1e9 (a range of four or eight neighbours taken out), or a bias of 1e9 or
+// +inf that forces an expert, leaves the other keys a few steps, and every
+// token goes to order_in_64: 16384 tokens, 128 experts, logits masked by -1e9
+// 134 us, by -1e4 13 us, by -inf or the type's lowest value 11 us; a forced
+// expert 228 us.
 #include <limits.h>
 #include <math.h>
 
@@ -80,7 +87,9 @@ __device__ __forceinline__ float warp_max(float v) { return unordered(__reduce_m
 
 // exp(x) and 1 / x in one instruction each beside the product with log2 e:
 // within 4 units of 2^-24 and the rounding of the argument, and 2 units;
-// results below the normal range are 0.
+// results below the normal range are 0. (The keys' error bound counts this. In
+// the full gradient of a softmax it shows far below the largest logit alone:
+// 5e-6 relative at 80 below, 0 from 87.4 below.)
 __device__ __forceinline__ float quick_exp(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.4426950408889634f));

@@ -209,7 +209,9 @@ int moe_device_status(int32_t* status, int clear);
  * give up at once: the kernel records MOE_ERR_TIMEOUT for moe_device_status,
  * leaves the output rows it did not finish unwritten and returns, with the
  * context still usable. A block always waits, with the full second, for the
- * copies it issued before it exits, so no copy lands after it. Process-wide
+ * copies it issued before it exits, so no copy lands after it (a block of the
+ * experts' products, whose copies are counted at the other block's barriers,
+ * waits two milliseconds). Process-wide
  * (every device), host only, does not synchronise. Always returns MOE_OK. */
 int moe_set_wait_limit_ns(uint64_t ns);
 
@@ -602,7 +604,8 @@ typedef struct {
  *   s       softmax(x) over the experts not taken out, or sigmoid(x)
  *   key     s + bias, compared as in 64-bit arithmetic; without a bias the
  *           experts are ordered by x itself, which orders as s does. A bias of
- *           -inf or NaN takes an expert out of the choice (not of the softmax).
+ *           -inf or NaN takes an expert out of the choice (not of the softmax),
+ *           one of +inf puts it before all that have none.
  *   groups  (G > 1) group g holds experts [g*E/G, (g+1)*E/G) and counts as its
  *           largest key or the sum of its two largest (of s where there is no
  *           bias; a missing second counts as 0); the topk_groups groups with
@@ -614,7 +617,10 @@ typedef struct {
  * Where fewer than k experts are left, the remaining ids are -1 (which every
  * call above takes as "no expert") and their weights 0; a token without any
  * gets a row of -1. Scores, sums and weights are fp32; where the fp32 keys
- * cannot tell the order for certain, it is settled in fp64.
+ * cannot tell the order for certain, it is settled in fp64. (Experts are best
+ * taken out by -inf or the type's lowest value. Beside finite masks like -1e9,
+ * or a bias as large, the other keys lie too close together for fp32, and the
+ * choice takes up to 30 times as long.)
  * Inputs (device): logits fp32 or bf16 [N, E]; bias fp32 [E] or NULL.
  * Outputs (device): topk_idx int32 [N, k]; topk_weights fp32 [N, k].
  * Pointers aligned to their element; 16-byte aligned rows are read faster.
@@ -655,8 +661,8 @@ typedef struct {
  * NULL) limits the work to rows below *num_rows, e.g. &expert_offset[E]; the
  * other rows are not touched. Arithmetic is fp32 with one rounding. An
  * infinity takes its group of 128 with it in the checkpoint (its scale is
- * infinite), NaN only itself. bf16 buffers 16-byte aligned, ckpt 8-byte. Errors: INVALID_ARG, SHAPE, ALIGNMENT,
- * CUDA. */
+ * infinite), NaN only itself. bf16 buffers 16-byte aligned, ckpt 8-byte.
+ * Errors: INVALID_ARG, SHAPE, ALIGNMENT, CUDA. */
 int moe_swiglu(const moe_glu_desc_t* desc, const int32_t* num_rows, const void* gate_up, void* act, void* ckpt,
                float* ckpt_scales, moe_stream_t stream);
 

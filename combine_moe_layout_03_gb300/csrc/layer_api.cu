@@ -1,6 +1,6 @@
 // layer_api.cu -- the extern "C" entry points of the router, the gated
-// activation and the experts' products (declared and documented in
-// include/moe.h): argument validation on the host, then the launches.
+// activation, the experts' products and their 8-bit forms (declared and
+// documented in include/moe.h): argument validation on the host, then the launches.
 #include <math.h>
 
 #include "moe_internal.cuh"
@@ -64,6 +64,56 @@ int check_expert(const moe_expert_desc_t* d, const int32_t* row_begin, const int
   p->row_end = row_end;
   p->rows = d->rows;
   p->x_stride = d->x_stride ? d->x_stride : d->in_features;
+  p->num_experts = d->num_experts;
+  p->in_features = d->in_features;
+  p->out_features = d->out_features;
+  return MOE_OK;
+}
+
+int check_quant(const moe_quant_desc_t* d, const int32_t* num_rows, moe::QuantParams* p) {
+  if (!d) return MOE_ERR_INVALID_ARG;
+  if (d->rows < 0 || d->rows >= ((int64_t)1 << 31) || d->width < 16 || d->width > 65536 || d->width % 16)
+    return MOE_ERR_SHAPE;
+  if (d->x_stride != 0 && (d->x_stride < d->width || d->x_stride % 8 || d->x_stride >= ((int64_t)1 << 36)))
+    return MOE_ERR_SHAPE;
+  if (d->scale_stride != 0 && d->scale_stride != 1 && d->scale_stride != 4) return MOE_ERR_SHAPE;
+  if (d->x_kind != MOE_ROWS_BF16 && d->x_kind != MOE_ROWS_F32) return MOE_ERR_INVALID_ARG;
+  if (!aligned(num_rows, 4)) return MOE_ERR_ALIGNMENT;
+  p->num_rows = num_rows;
+  p->rows = d->rows;
+  p->x_stride = d->x_stride ? d->x_stride : d->width;
+  p->width = d->width;
+  p->x_kind = d->x_kind;
+  p->scale_stride = d->scale_stride == 4 ? 4 : 1;
+  return MOE_OK;
+}
+
+int check_expert_i8(const moe_expert_i8_desc_t* d, const void* x, const float* x_scales, const int32_t* row_begin,
+                    const int32_t* row_end, const void* w, const float* w_scales, void* out, moe::ExpertI8Params* p) {
+  if (!d) return MOE_ERR_INVALID_ARG;
+  if (d->num_experts < 1 || d->num_experts > MOE_MAX_EXPERTS) return MOE_ERR_SHAPE;
+  if (d->rows < 0 || d->rows >= ((int64_t)1 << 31) - 128) return MOE_ERR_SHAPE;
+  if (d->in_features < 16 || d->in_features > 65536 || d->in_features % 16) return MOE_ERR_SHAPE;
+  if (d->out_features < 8 || d->out_features > 65536 || d->out_features % 8) return MOE_ERR_SHAPE;
+  if (d->x_stride != 0 && (d->x_stride < d->in_features || d->x_stride % 16 || d->x_stride >= ((int64_t)1 << 36)))
+    return MOE_ERR_SHAPE;
+  if (d->x_scale_stride < 0 || d->x_scale_stride >= ((int64_t)1 << 36)) return MOE_ERR_SHAPE;
+  if (!row_begin || !row_end) return MOE_ERR_INVALID_ARG;
+  if (!aligned(row_begin, 4) || !aligned(row_end, 4)) return MOE_ERR_ALIGNMENT;
+  p->rows = d->rows;
+  if (p->rows == 0) return MOE_OK;
+  if (!x || !x_scales || !w || !w_scales || !out) return MOE_ERR_INVALID_ARG;
+  if (!aligned(x, 16) || !aligned(w, 16) || !aligned(out, 16) || !aligned(x_scales, 4) || !aligned(w_scales, 4))
+    return MOE_ERR_ALIGNMENT;
+  p->row_begin = row_begin;
+  p->row_end = row_end;
+  p->x = (const int8_t*)x;
+  p->x_scales = x_scales;
+  p->w = (const int8_t*)w;
+  p->w_scales = w_scales;
+  p->out = (uint8_t*)out;
+  p->x_stride = d->x_stride ? d->x_stride : d->in_features;
+  p->x_scale_stride = d->x_scale_stride ? d->x_scale_stride : 1;
   p->num_experts = d->num_experts;
   p->in_features = d->in_features;
   p->out_features = d->out_features;
@@ -203,6 +253,35 @@ int moe_expert_product_backward_weight(const moe_expert_desc_t* desc, const void
     return cuda_status(cudaMemsetAsync(grad_w, 0, bytes, (cudaStream_t)stream));
   }
   return cuda_status(moe::launch_expert_grad_weight(p, (cudaStream_t)stream));
+}
+
+int moe_quantize_rows(const moe_quant_desc_t* desc, const int32_t* num_rows, const void* x, int8_t* q, float* scales,
+                      moe_stream_t stream) {
+  moe::QuantParams p = {};
+  int rc = check_quant(desc, num_rows, &p);
+  if (rc != MOE_OK || p.rows == 0) return rc;
+  if (!x || !q || !scales) return MOE_ERR_INVALID_ARG;
+  if (!aligned(x, 16) || !aligned(q, 16) || !aligned(scales, p.scale_stride == 4 ? 16 : 4)) return MOE_ERR_ALIGNMENT;
+  p.x = (const uint8_t*)x;
+  p.q = q;
+  p.scales = scales;
+  return cuda_status(moe::launch_quantize(p, (cudaStream_t)stream));
+}
+
+int moe_expert_product_i8(const moe_expert_i8_desc_t* desc, const int8_t* x, const float* x_scales, const int32_t* row_begin,
+                          const int32_t* row_end, const int8_t* w, const float* w_scales, void* y, moe_stream_t stream) {
+  moe::ExpertI8Params p = {};
+  int rc = check_expert_i8(desc, x, x_scales, row_begin, row_end, w, w_scales, y, &p);
+  if (rc != MOE_OK || p.rows == 0) return rc;
+  return cuda_status(moe::launch_expert_product_i8(p, (cudaStream_t)stream));
+}
+
+int moe_expert_swiglu_i8(const moe_expert_i8_desc_t* desc, const int8_t* x, const float* x_scales, const int32_t* row_begin,
+                         const int32_t* row_end, const int8_t* w, const float* w_scales, void* act, moe_stream_t stream) {
+  moe::ExpertI8Params p = {};
+  int rc = check_expert_i8(desc, x, x_scales, row_begin, row_end, w, w_scales, act, &p);
+  if (rc != MOE_OK || p.rows == 0) return rc;
+  return cuda_status(moe::launch_expert_swiglu_i8(p, (cudaStream_t)stream));
 }
 
 }  // extern "C"

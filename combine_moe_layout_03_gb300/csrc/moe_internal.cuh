@@ -171,6 +171,27 @@ struct ExpertParams {
   int grad_kind;             // MOE_GRAD_*
 };
 
+struct QuantParams {
+  const int32_t* num_rows;  // device row count, or null
+  const uint8_t* x;         // bf16 or fp32 [rows, x_stride]
+  int8_t* q;                // [rows, width]
+  float* scales;            // [rows, scale_stride]
+  int64_t rows, x_stride;
+  int width, x_kind, scale_stride;
+};
+
+struct ExpertI8Params {
+  const int32_t* row_begin;  // [E]
+  const int32_t* row_end;    // [E]
+  const int8_t* x;           // [rows, x_stride]
+  const float* x_scales;     // [rows, x_scale_stride]
+  const int8_t* w;           // [E, N, K], of the gated product [E, 2N, K]
+  const float* w_scales;     // [E, N] or [E, 2N]
+  uint8_t* out;              // bf16 [rows, N]
+  int64_t rows, x_stride, x_scale_stride;
+  int num_experts, in_features, out_features;
+};
+
 // Programmatic dependent launch. Every kernel of this library begins with
 // pdl_wait() -- griddepcontrol.wait: until the previous kernel in the stream
 // has completed and its memory operations are visible -- before its first
@@ -260,6 +281,9 @@ cudaError_t launch_expert_product(const ExpertParams& p, cudaStream_t s);
 cudaError_t launch_expert_swiglu(const ExpertParams& p, cudaStream_t s);
 cudaError_t launch_expert_grad_input(const ExpertParams& p, cudaStream_t s);
 cudaError_t launch_expert_grad_weight(const ExpertParams& p, cudaStream_t s);
+cudaError_t launch_quantize(const QuantParams& p, cudaStream_t s);
+cudaError_t launch_expert_product_i8(const ExpertI8Params& p, cudaStream_t s);
+cudaError_t launch_expert_swiglu_i8(const ExpertI8Params& p, cudaStream_t s);
 
 #ifdef __CUDACC__
 

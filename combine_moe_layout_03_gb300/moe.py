@@ -48,6 +48,9 @@ MOE_GRAD_BF16 = 0
 MOE_GRAD_F32 = 1
 MOE_GRAD_F32_ADD = 2
 
+MOE_ROWS_BF16 = 0
+MOE_ROWS_F32 = 1
+
 if not os.path.exists(LIB_PATH):
     raise ImportError(
         f"{LIB_PATH} is missing: build it with `python -c \"import __graft_entry__ as g; g.build()\"` "
@@ -153,12 +156,23 @@ class _ExpertDesc(ctypes.Structure):
                 ("out_features", _i32)]
 
 
+class _QuantDesc(ctypes.Structure):
+    _fields_ = [("rows", _i64), ("x_stride", _i64), ("width", _i32), ("x_kind", _i32), ("scale_stride", _i32)]
+
+
+class _ExpertI8Desc(ctypes.Structure):
+    _fields_ = [("rows", _i64), ("x_stride", _i64), ("x_scale_stride", _i64), ("num_experts", _i32),
+                ("in_features", _i32), ("out_features", _i32)]
+
+
 for _name, _desc, _args in (
         ("moe_route", _RouteDesc, [_vp] * 5), ("moe_route_backward", _RouteDesc, [_vp] * 5),
         ("moe_swiglu", _GluDesc, [_vp] * 6), ("moe_swiglu_backward", _GluDesc, [_vp] * 7),
         ("moe_expert_product", _ExpertDesc, [_vp] * 6), ("moe_expert_swiglu", _ExpertDesc, [_vp] * 8),
         ("moe_expert_product_backward_input", _ExpertDesc, [_vp] * 6),
-        ("moe_expert_product_backward_weight", _ExpertDesc, [_vp] * 5 + [ctypes.c_int, _vp])):
+        ("moe_expert_product_backward_weight", _ExpertDesc, [_vp] * 5 + [ctypes.c_int, _vp]),
+        ("moe_quantize_rows", _QuantDesc, [_vp] * 5),
+        ("moe_expert_product_i8", _ExpertI8Desc, [_vp] * 8), ("moe_expert_swiglu_i8", _ExpertI8Desc, [_vp] * 8)):
     getattr(_lib, _name).restype = ctypes.c_int
     getattr(_lib, _name).argtypes = [ctypes.POINTER(_desc)] + _args
 
@@ -873,6 +887,38 @@ class MoeExpertDesc:
         return _ExpertDesc(self.rows, self.x_stride, self.num_experts, self.in_features, self.out_features)
 
 
+@dataclass
+class MoeQuantDesc:
+    """Shape and format of one moe_quantize_rows call (moe_quant_desc_t)."""
+    rows: int
+    width: int
+    x_kind: int = MOE_ROWS_BF16
+    x_stride: int = 0
+    scale_stride: int = 1
+
+    def c(self) -> _QuantDesc:
+        return _QuantDesc(self.rows, self.x_stride, self.width, self.x_kind, self.scale_stride)
+
+    @property
+    def x_dtype(self):
+        return torch.float32 if self.x_kind == MOE_ROWS_F32 else torch.bfloat16
+
+
+@dataclass
+class MoeExpertI8Desc:
+    """Shape of one call of the experts' 8-bit products (moe_expert_i8_desc_t)."""
+    num_experts: int
+    rows: int
+    in_features: int
+    out_features: int
+    x_stride: int = 0
+    x_scale_stride: int = 0
+
+    def c(self) -> _ExpertI8Desc:
+        return _ExpertI8Desc(self.rows, self.x_stride, self.x_scale_stride, self.num_experts, self.in_features,
+                             self.out_features)
+
+
 def _fresh(shape, dtype, device, stream):
     """An output of a call on `stream`, out of that stream's memory: a block of the current stream's may still be
     written by what is queued there."""
@@ -1123,6 +1169,70 @@ def moe_expert_product_backward_weight(desc: MoeExpertDesc, grad_y, x, row_begin
     return grad_w
 
 
+def prepare_quantize_rows(desc: MoeQuantDesc, x, q, scales, num_rows=None, stream=None) -> Prepared:
+    r, n = desc.rows, desc.width
+    _want("num_rows", num_rows, torch.int32, 1, optional=True)
+    _want_rows("x", x, desc.x_dtype, r, n, desc.x_stride or n)
+    _want("q", q, torch.int8, r * n)
+    _want("scales", scales, torch.float32, r * (desc.scale_stride or 1))
+    d = desc.c()
+    args = (ctypes.byref(d), *_vps(num_rows, x, q, scales), ctypes.c_void_p(_stream(stream)))
+    return Prepared("moe_quantize_rows", args, (d, num_rows, x, q, scales))
+
+
+def moe_quantize_rows(desc: MoeQuantDesc, x, q=None, scales=None, num_rows=None, stream=None):
+    """Rows to 8-bit integers with a scale each (see include/moe.h).
+    Returns (q int8 [rows, width], scales fp32 [rows, scale_stride])."""
+    if q is None:
+        q = _fresh((desc.rows, desc.width), torch.int8, x.device, stream)
+    if scales is None:
+        scales = _fresh((desc.rows, desc.scale_stride or 1), torch.float32, x.device, stream)
+    prepare_quantize_rows(desc, x, q, scales, num_rows, stream)()
+    return q, scales
+
+
+def _prepare_expert_i8(name: str, desc: MoeExpertI8Desc, halves: int, x, x_scales, row_begin, row_end, w, w_scales, out,
+                       stream) -> Prepared:
+    e, r, k, n = desc.num_experts, desc.rows, desc.in_features, desc.out_features
+    _want("row_begin", row_begin, torch.int32, e)
+    _want("row_end", row_end, torch.int32, e)
+    _want_rows("x", x, torch.int8, r, k, desc.x_stride or k)
+    _want_rows("x_scales", x_scales, torch.float32, r, 1, desc.x_scale_stride or 1)
+    _want("w", w, torch.int8, e * halves * n * k)
+    _want("w_scales", w_scales, torch.float32, e * halves * n)
+    _want("act" if halves == 2 else "y", out, torch.bfloat16, r * n)
+    d = desc.c()
+    args = (ctypes.byref(d), *_vps(x, x_scales, row_begin, row_end, w, w_scales, out), ctypes.c_void_p(_stream(stream)))
+    return Prepared(name, args, (d, x, x_scales, row_begin, row_end, w, w_scales, out))
+
+
+def prepare_expert_product_i8(desc: MoeExpertI8Desc, x, x_scales, row_begin, row_end, w, w_scales, y,
+                              stream=None) -> Prepared:
+    return _prepare_expert_i8("moe_expert_product_i8", desc, 1, x, x_scales, row_begin, row_end, w, w_scales, y, stream)
+
+
+def moe_expert_product_i8(desc: MoeExpertI8Desc, x, x_scales, row_begin, row_end, w, w_scales, y=None, stream=None):
+    """y[s] = w[e] x[s] for int8 rows and weights, with their scales (see include/moe.h). Returns y bf16 [rows, N]."""
+    if y is None:
+        y = _fresh((desc.rows, desc.out_features), torch.bfloat16, w.device, stream)
+    prepare_expert_product_i8(desc, x, x_scales, row_begin, row_end, w, w_scales, y, stream)()
+    return y
+
+
+def prepare_expert_swiglu_i8(desc: MoeExpertI8Desc, x, x_scales, row_begin, row_end, w, w_scales, act,
+                             stream=None) -> Prepared:
+    return _prepare_expert_i8("moe_expert_swiglu_i8", desc, 2, x, x_scales, row_begin, row_end, w, w_scales, act, stream)
+
+
+def moe_expert_swiglu_i8(desc: MoeExpertI8Desc, x, x_scales, row_begin, row_end, w, w_scales, act=None, stream=None):
+    """silu(gate) * up with gate|up = w[e] x[s] as in moe_expert_product_i8, w int8 [E, 2F, K], desc.out_features = F.
+    Returns act bf16 [rows, F]."""
+    if act is None:
+        act = _fresh((desc.rows, desc.out_features), torch.bfloat16, w.device, stream)
+    prepare_expert_swiglu_i8(desc, x, x_scales, row_begin, row_end, w, w_scales, act, stream)()
+    return act
+
+
 def exported_symbols() -> list[str]:
     return ["moe_strerror", "moe_record_layout", "moe_workspace_size", "moe_layout",
             "moe_layout_status", "moe_dispatch", "moe_combine", "moe_pack_record",
@@ -1133,4 +1243,5 @@ def exported_symbols() -> list[str]:
             "moe_combine_gather_ranks_backward", "moe_layout_dispatch", "moe_device_status",
             "moe_layout_ranks", "moe_layout_ll", "moe_layout_ll_dispatch", "moe_set_wait_limit_ns",
             "moe_route", "moe_route_backward", "moe_swiglu", "moe_swiglu_backward", "moe_expert_product",
-            "moe_expert_swiglu", "moe_expert_product_backward_input", "moe_expert_product_backward_weight"]
+            "moe_expert_swiglu", "moe_expert_product_backward_input", "moe_expert_product_backward_weight",
+            "moe_quantize_rows", "moe_expert_product_i8", "moe_expert_swiglu_i8"]

@@ -30,7 +30,8 @@
  * kernels; the backward of combine and dispatch; the decode all-gather's
  * rank-slot packing and padded-token mask; an allocation-free layout; the
  * router, the experts' products and the gated activation with its 8-bit
- * checkpoint, which complete an MoE layer around dispatch and combine.
+ * checkpoint, which complete an MoE layer around dispatch and combine; rows
+ * rounded to 8-bit integers and the experts' products of them, for serving.
  *
  * Conventions
  *  - Every function returns an int status: MOE_OK (0) or a negative MOE_ERR_*
@@ -729,6 +730,69 @@ int moe_expert_product_backward_input(const moe_expert_desc_t* desc, const void*
 int moe_expert_product_backward_weight(const moe_expert_desc_t* desc, const void* grad_y, const void* x,
                                        const int32_t* row_begin, const int32_t* row_end, void* grad_w,
                                        int grad_kind, moe_stream_t stream);
+
+/* ---- experts in 8-bit integers ---------------------------------------------
+ * For serving: weights and rows held in int8, a weight matrix with one fp32
+ * scale for each output channel and a row with one for itself. moe_quantize_rows
+ * makes both (a weight matrix's rows are its channels). Rounded tokens travel as
+ * RAW records (raw_payload_bytes = H, raw_scale_bytes = 16 with scale_stride = 4),
+ * out of which the first product reads them. Training keeps to the bf16 calls
+ * above, which have gradients. */
+#define MOE_ROWS_BF16 0
+#define MOE_ROWS_F32 1
+typedef struct {
+  int64_t rows;         /* rows of the buffers, in [0, 2^31) */
+  int64_t x_stride;     /* elements between rows of x, >= width, % 8 == 0 (0: width) */
+  int32_t width;        /* elements of a row, % 16 == 0, in [16, 65536] */
+  int32_t x_kind;       /* MOE_ROWS_* */
+  int32_t scale_stride; /* floats between rows of scales: 1, or 4 for 16 bytes a row (0: 1) */
+} moe_quant_desc_t;
+
+/* Rows of bf16 or fp32 to int8, each with its scale:
+ *   a = max(max_k |x[r, k]|, 1e-30)
+ *   q[r, k] = rint(x[r, k] * (127 / a))      (halves to the even number)
+ *   scale[r] = a / 127
+ * in IEEE fp32, each operation rounded by itself, so that results are the same
+ * bit for bit wherever they are computed. Codes are in [-127, 127]; a row of
+ * zeros has codes 0. A row that holds NaN or an infinity gets codes 0 and the
+ * scale NaN, which the products below carry into the whole row.
+ * x [rows, width] (x_stride), q int8 [rows, width], scales fp32 [rows,
+ * scale_stride]; with scale_stride 4 the three floats behind a scale are set to
+ * zero. num_rows (device int32, may be NULL) limits the work to rows below
+ * *num_rows; the other rows are not touched. x and q 16-byte aligned, scales
+ * too with scale_stride 4. Errors: INVALID_ARG, SHAPE, ALIGNMENT, CUDA. */
+int moe_quantize_rows(const moe_quant_desc_t* desc, const int32_t* num_rows, const void* x, int8_t* q, float* scales,
+                      moe_stream_t stream);
+
+typedef struct {
+  int64_t rows;           /* rows of the row buffers, in [0, 2^31 - 128) */
+  int64_t x_stride;       /* bytes between rows of x, >= in_features, % 16 == 0 (0: in_features) */
+  int64_t x_scale_stride; /* floats between the scales of rows, in [1, 2^36) (0: 1) */
+  int32_t num_experts;    /* E in [1, 1024] */
+  int32_t in_features;    /* K, % 16 == 0, in [16, 65536] */
+  int32_t out_features;   /* N, % 8 == 0, in [8, 65536]; of moe_expert_swiglu_i8: F, the width of act */
+} moe_expert_i8_desc_t;
+
+/* y[s, n] = bf16_rn( (sum_k x[s, k] * w[e, n, k]) * (x_scales[s] * w_scales[e, n]) )
+ * for s in expert e's rows [row_begin[e], row_end[e]), as moe_expert_product
+ * takes them. x int8 [rows, K] (x_stride), x_scales fp32 (x_scale_stride), w int8
+ * [E, N, K], w_scales fp32 [E, N], y bf16 [rows, N]. Any int8 value is taken, -128
+ * too. Sums of whole numbers are exact while they and their parts stay within
+ * 2^24 in magnitude, and fp32 sums beyond; the two factors are fp32 products.
+ * A scale that is NaN makes its row or channel NaN. For rows out of RAW records:
+ * x = records + off_payload with x_stride = record_bytes, x_scales = records +
+ * off_scales with x_scale_stride = record_bytes / 4. x, w and y 16-byte aligned,
+ * scales 4-byte. The waits inside are bounded as moe_device_status describes.
+ * Errors: INVALID_ARG, SHAPE, ALIGNMENT, CUDA. */
+int moe_expert_product_i8(const moe_expert_i8_desc_t* desc, const int8_t* x, const float* x_scales, const int32_t* row_begin,
+                          const int32_t* row_end, const int8_t* w, const float* w_scales, void* y, moe_stream_t stream);
+
+/* The first product with the activation in its epilogue: w int8 [E, 2F, K]
+ * (gate rows, then up rows), w_scales fp32 [E, 2F], act bf16 [rows, F] =
+ * silu(gate) * up from the scaled fp32 sums, which are not rounded in between.
+ * Errors: as moe_expert_product_i8. */
+int moe_expert_swiglu_i8(const moe_expert_i8_desc_t* desc, const int8_t* x, const float* x_scales, const int32_t* row_begin,
+                         const int32_t* row_end, const int8_t* w, const float* w_scales, void* act, moe_stream_t stream);
 
 #ifdef __cplusplus
 }

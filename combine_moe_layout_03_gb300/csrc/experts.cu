@@ -41,11 +41,9 @@
 // rows take 670 to 725 us in long runs. Few rows: the weights, 8 rows an expert
 // 274 to 283 us for 1.88 GB (6.9 TB/s). Weight gradients: their result, 3.76 GB
 // of fp32 780 to 880 us (bf16 695 to 705, added to fp32 1483).
-#include <cuda.h>
-
 #include <mutex>
 
-#include "moe_internal.cuh"
+#include "tcgen05.cuh"
 
 namespace moe {
 
@@ -69,100 +67,6 @@ constexpr int kBoxes = 2;                    // of each warp
 constexpr int stages_of(int mode) { return mode == kGradWeight ? 5 : 6; }
 
 __device__ int32_t g_expert_status;  // MOE_OK, or MOE_ERR_TIMEOUT once a wait gave up
-
-// ---- clusters, tcgen05 and TMA ------------------------------------------------
-
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// One lane of a warp that runs together. The operations below that one thread
-// issues are predicated on it instead of standing behind a branch: the warp
-// then stays together and their operands in uniform registers. (Behind `if
-// (lane == 0)` two copies took 680 cycles a step, more than the products.)
-__device__ __forceinline__ uint32_t elect_one() {
-  uint32_t on;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(on));
-  return on;
-}
-// The address of a shared variable in block `rank` of the cluster.
-__device__ __forceinline__ uint32_t in_block(const void* p, uint32_t rank) {
-  uint32_t a;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
-  return a;
-}
-// What this thread wrote is visible to whoever waits with wait_cluster.
-__device__ __forceinline__ void arrive_at(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-// A release to this block alone. To the other block it hands over no memory,
-// only tensor memory that has been read (after tmem_fence_before).
-__device__ __forceinline__ void arrive_local_at(uint32_t bar, uint32_t on) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %1, 0;\n\t@p mbarrier.arrive.shared::cluster.b64 _, [%0];\n\t}" ::"r"(bar),
-      "r"(on)
-      : "memory");
-}
-// What this warp wrote to its block's shared memory is visible to whoever waits
-// with wait_cluster. All lanes come; those with `on` arrive. The fence covers
-// shared memory alone: arrive_at would wait for all that the block has under
-// way, stores to global memory too (at the end of each ragged reduction, 165
-// of 940 us).
-__device__ __forceinline__ void arrive_with_shared_at(uint32_t bar, uint32_t on) {
-  __syncwarp();
-  asm volatile("fence.release.sync_restrict::shared::cta.cluster;" ::: "memory");
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %1, 0;\n\t"
-      "@p mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];\n\t}" ::"r"(bar),
-      "r"(on)
-      : "memory");
-}
-// Announces copies; it orders nothing else, and a release here would wait for
-// all that the thread has under way, at every step.
-__device__ __forceinline__ void arrive_expect_at(uint32_t bar, uint32_t bytes, uint32_t on) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\t"
-      "@p mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;\n\t}" ::"r"(bar),
-      "r"(bytes), "r"(on)
-      : "memory");
-}
-// mbar_wait where what the other block wrote before it arrived is read next.
-// (Copies and MMAs need no such order, and it costs most of a microsecond.)
-__device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity, uint64_t limit_ns = kWaitLimitNs) {
-  uint64_t t0 = 0;
-  while (true) {
-    uint32_t ok;
-    if (limit_ns < kWaitLimitNs)  // a lowered budget (test hook): poll without suspending
-      asm volatile(
-          "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-          "selp.u32 %0, 1, 0, p;\n\t}"
-          : "=r"(ok)
-          : "r"(smem_u32(bar)), "r"(parity)
-          : "memory");
-    else
-      asm volatile(
-          "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-          "selp.u32 %0, 1, 0, p;\n\t}"
-          : "=r"(ok)
-          : "r"(smem_u32(bar)), "r"(parity)
-          : "memory");
-    if (ok) return true;
-    const uint64_t now = global_timer_ns();
-    if (t0 == 0) t0 = now;
-    if (now - t0 > limit_ns) return false;
-  }
-}
-// All lanes wait, and leave together.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, limit_ns));
-}
-__device__ __forceinline__ bool warp_wait_cluster(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
-  return __all_sync(0xffffffffu, wait_cluster(bar, parity, limit_ns));
-}
 
 // The same where what is waited for may be as far away as an expert's last row
 // (a weight gradient reduces over all of them): the budget is for one step. It
@@ -200,32 +104,6 @@ __device__ __forceinline__ bool epilogue_agrees(bool yes) {
   return all != 0;
 }
 
-// Box into this block's shared memory; the bytes are counted at bar, in either
-// block of the pair.
-__device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, int x, int y, uint32_t bar, uint32_t on) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\t"
-      "@p cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 "
-      "[%0], [%1, {%2, %3}], [%4];\n\t}" ::"r"(smem_u32(dst)),
-      "l"(map), "r"(x), "r"(y), "r"(bar), "r"(on)
-      : "memory");
-}
-__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar, uint32_t on) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
-      "@p cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 "
-      "[%0], [%1, {%2, %3, %4}], [%5];\n\t}" ::"r"(smem_u32(dst)),
-      "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar), "r"(on)
-      : "memory");
-}
-__device__ __forceinline__ void tma_load_5d(void* dst, const CUtensorMap* map, int x, int y, int z, int v, int w, uint32_t bar, uint32_t on) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %8, 0;\n\t"
-      "@p cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 "
-      "[%0], [%1, {%2, %3, %4, %5, %6}], [%7];\n\t}" ::"r"(smem_u32(dst)),
-      "l"(map), "r"(x), "r"(y), "r"(z), "r"(v), "r"(w), "r"(bar), "r"(on)
-      : "memory");
-}
 // (evict-first: written once and read by another kernel later; it takes 3 to 8%
 // off weight gradients of few rows)
 __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void* src, int x, int y, int z, uint32_t on) {
@@ -242,67 +120,6 @@ __device__ __forceinline__ void tma_add_3d(const CUtensorMap* map, const void* s
       "@p cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2, %3}], [%4];\n\t}" ::"l"(map),
       "r"(x), "r"(y), "r"(z), "r"(smem_u32(src)), "r"(on)
       : "memory");
-}
-__device__ __forceinline__ void tmem_alloc(uint32_t* dst, uint32_t columns) {
-  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst)), "r"(columns)
-               : "memory");
-  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
-}
-__device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t columns) {
-  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(columns));
-}
-__device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add, uint32_t on) {
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-      "@q tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add), "r"(on)
-      : "memory");
-}
-// Arrives on bar in both blocks when every MMA issued so far by this thread has completed.
-__device__ __forceinline__ void mma_commit(uint64_t* bar, uint32_t on) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\t"
-      "@p tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(
-          smem_u32(bar)),
-      "h"((uint16_t)3), "r"(on)
-      : "memory");
-}
-__device__ __forceinline__ void tmem_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tmem_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-
-// 32 lanes x 32 columns of fp32: lane l of the warp gets tensor-memory lane
-// (warp % 4) * 32 + l, columns [addr, addr + 32).
-__device__ __forceinline__ void tmem_load32(uint32_t addr, float (&v)[32]) {
-  uint32_t r[32];
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(addr));
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-}
-
-// Shared-memory operand descriptor, 128-byte swizzle (16-byte units: start in
-// bits 0-13, leading stride in 16-29, stride in 32-45; bit 46 set; swizzle in
-// 61-63). An atom is 8 rows of 128 bytes = 1024 bytes.
-//  K-major: rows are the M or N index; the next 8 rows follow at 1024 bytes.
-//  MN-major: rows are reduction steps, 64 M or N indices each; the next 8
-//  steps follow at 1024 bytes, the next 64 indices at 64 rows = 8192 bytes.
-__device__ __forceinline__ uint64_t operand_desc(uint32_t addr, bool mn_major) {
-  const uint64_t lead = mn_major ? 8192 / 16 : 1, stride = 1024 / 16;
-  return (uint64_t)((addr >> 4) & 0x3fff) | lead << 16 | stride << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
-}
-// Instruction descriptor: fp32 accumulators (bit 4), bf16 A and B (bits 7 and
-// 10), MN-major A and B (bits 15 and 16), N / 8 in bits 17-22, M / 16 in 24-28.
-__device__ __forceinline__ uint32_t instr_desc(bool a_mn, bool b_mn, int n) {
-  return 1u << 4 | 1u << 7 | 1u << 10 | (a_mn ? 1u << 15 : 0) | (b_mn ? 1u << 16 : 0) | (uint32_t)(n / 8) << 17 |
-         (uint32_t)(kTileM / 16) << 24;
 }
 
 struct ExpertMaps {
@@ -336,13 +153,6 @@ constexpr size_t expert_smem(int mode, int experts) {
          (mode == kGradWeight ? 0 : ((size_t)experts + 1) * 4) + sizeof(ExpertControl) + 16;
 }
 
-template <int STAGES>
-__device__ __forceinline__ void next_stage(int& st, uint32_t& phase) {
-  if (++st == STAGES) {
-    st = 0;
-    phase ^= 1u;
-  }
-}
 
 // Row tiles of an expert: as few as hold its rows, of equal width in steps of
 // 32; the last is as wide as what is left.
@@ -586,7 +396,7 @@ __global__ void __launch_bounds__(kExpertThreads, 1)
         break;
       }
       tmem_fence_after();
-      const uint32_t idesc = instr_desc(a_mn, b_mn, o.n);
+      const uint32_t idesc = instr_desc(true, a_mn, b_mn, kTileM, o.n);
       for (int k = 0; k < steps; ++k, next_stage<kStages>(st, phase)) {
         uint8_t* a = stages + st * kStageBytes;
         int parts = kTileK / 16;
@@ -829,25 +639,6 @@ __global__ void __launch_bounds__(kExpertThreads, 1)
   if (warp == 1) tmem_free(tmem, kTmemColumns);
   __syncwarp();
   cluster_sync();  // and neither leaves before both have freed theirs
-}
-
-// cuTensorMapEncodeTiled, looked up once (the library links no driver stub).
-using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-EncodeTiled encode_tiled() {
-  static const EncodeTiled fn = [] {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult found;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found) !=
-            cudaSuccess ||
-        found != cudaDriverEntryPointSuccess) {
-      cudaGetLastError();
-      f = nullptr;
-    }
-    return (EncodeTiled)f;
-  }();
-  return fn;
 }
 
 // Tensor [depth][rows][width] (two dimensions where depth is 0) of bf16 or

@@ -714,9 +714,10 @@ int read_device_status(int32_t* out, bool clear) {
       return MOE_ERR_CUDA;
     }
   }
-  int32_t ve = 0;  // the experts' kernels keep a word of their own
-  const int rc = read_expert_status(&ve, clear);
-  *out = v != 0 ? v : ve;
+  int32_t ve = 0, v8 = 0;  // the experts' kernels keep words of their own
+  int rc = read_expert_status(&ve, clear);
+  if (rc == MOE_OK) rc = read_expert_i8_status(&v8, clear);
+  *out = v != 0 ? v : ve != 0 ? ve : v8;
   return rc;
 }
 

@@ -1,75 +1,528 @@
-// experts_i8.cu -- the experts' products of 8-bit integers.
+// experts_i8.cu -- the experts' products of 8-bit integers on the tensor cores.
 //
 //   product  y[s, n] = (sum_k x[s, k] w[e, n, k]) * (sx[s] * sw[e, n])
 //   swiglu   the same for gate and up rows of w, and silu(gate) * up
 //
-// A block walks over one expert's rows, 32 at a time, for 64 features; sums are
-// 32-bit integers.
-#include "moe_internal.cuh"
+// This chip's integer tensor rate is a fraction of its 16-bit float rate, so
+// whole numbers are multiplied as f16: every int8 is one exactly, products of
+// two are below 2^15 and their sums exact in the fp32 accumulators up to 2^24.
+// Operands travel and wait in 8 bits and become f16 on their way into the
+// tensor cores.
+//
+// A pair of blocks (a cluster of two, tcgen05 cta_group::2) walks over output
+// tiles as the bf16 products do: 256 features (M), 128 to a block, by up to 192
+// rows of one expert (N), in steps of 32. Warps 0 and 2 load features and rows
+// with TMA, 128 reduction steps at a time. Warps 4-7 turn features into f16 and
+// put them into tensor memory, from where the products take their M operand:
+// shared memory, which is what a step is short of (it would read and write 96 KB
+// of it, 64 KB this way), then holds them in 8 bits only. Warps 8-11 turn rows into
+// f16 in shared memory. Warp 1 of the even block issues tcgen05.mma for both,
+// 64 reduction steps at a time; warps 12-15 scale what is finished and store it.
+// Tensor memory holds two accumulators of 192 columns, so that a tile's
+// epilogue runs beside the next one's products, and four stages of features of
+// 32 columns.
+#include <mutex>
+
+#include "tcgen05.cuh"
 
 namespace moe {
 
 namespace {
 
-constexpr int kFeatures = 64, kRows = 32, kWords = 16, kThreads = 256;
+constexpr int kTileM = 256, kTileN = 192;     // of a pair
+constexpr int kHalfM = 128;                   // of a block
+constexpr int kLoadK = 128, kStepK = 64;      // reduction steps loaded together, and multiplied together
+constexpr int kLoads = 5, kSteps = 4;         // stages of each
+constexpr int kBytesA = kHalfM * kLoadK, kBytesB = kTileN / 2 * kLoadK, kLoadBytes = kBytesA + kBytesB;
+constexpr int kStepBytes = kTileN / 2 * kStepK * 2;  // rows as f16
+constexpr int kTmemColumns = 512;
+constexpr int kFeatureColumn = 2 * kTileN;    // of the first stage of features
+constexpr int kStageColumns = kStepK / 2;
+constexpr int kThreads = 512;
+constexpr int kChunk = 32;                    // rows that leave together
+constexpr int kChunkBytes = kChunk * 256;     // 128 features in bf16
 
-template <bool GLU>
-__global__ void __launch_bounds__(kThreads) k_expert_i8(ExpertI8Params p) {
-  constexpr int kHalves = GLU ? 2 : 1;
-  __shared__ int32_t ws[kHalves][kFeatures][kWords + 1], xs[kRows][kWords + 1];
-  pdl_wait();
-  pdl_trigger();
-  const int e = blockIdx.y, f0 = blockIdx.x * kFeatures, K = p.in_features, N = p.out_features;
-  const int64_t lo = max(p.row_begin[e], 0), hi = min((int64_t)max(p.row_end[e], 0), p.rows);
-  const int f = threadIdx.x & 63, part = threadIdx.x >> 6;  // eight rows to a thread
-  for (int64_t r0 = lo; r0 < hi; r0 += kRows) {
-    int32_t acc[kHalves][8] = {};
-    for (int k0 = 0; k0 < K; k0 += kWords * 4) {
-      __syncthreads();
-      for (int i = threadIdx.x; i < kHalves * kFeatures * kWords; i += kThreads) {
-        const int c = i % kWords, row = i / kWords % kFeatures, h = i / kWords / kFeatures;
-        int32_t v = 0;
-        if (f0 + row < N && k0 + c * 4 < K)
-          v = *reinterpret_cast<const int32_t*>(p.w + (((int64_t)e * kHalves + h) * N + f0 + row) * K + k0 + c * 4);
-        ws[h][row][c] = v;
-      }
-      for (int i = threadIdx.x; i < kRows * kWords; i += kThreads) {
-        const int c = i % kWords, row = i / kWords;
-        int32_t v = 0;
-        if (r0 + row < hi && k0 + c * 4 < K)
-          v = *reinterpret_cast<const int32_t*>(p.x + (r0 + row) * p.x_stride + k0 + c * 4);
-        xs[row][c] = v;
-      }
-      __syncthreads();
+__device__ int32_t g_expert_i8_status;  // MOE_OK, or MOE_ERR_TIMEOUT once a wait gave up
+
+struct Maps {
+  CUtensorMap a;     // features
+  CUtensorMap b[3];  // rows, in boxes of 16, 32 and 64
+};
+
+struct Tile {
+  int e, f0;     // expert, first feature
+  int n0, n;     // first row of the expert, and how many; n a multiple of 32
+  int lo, rows;  // the expert's rows
+};
+
+struct Control {
+  uint64_t loaded[kLoads], used[kLoads], full[kSteps], empty[kSteps], acc_full[2], acc_empty[2];
+  uint32_t tmem;
+  alignas(16) float row_scales[2][kTileN];  // read four at a time
+};
+constexpr size_t smem_bytes(int experts) {
+  return 1024 + (size_t)kLoads * kLoadBytes + (size_t)kSteps * kStepBytes + kChunkBytes + sizeof(Control) + ((size_t)experts + 1) * 4;
+}
+
+// Named barrier of the epilogue warps, and a vote at it. It waits without a
+// limit, so whoever comes must know that the others do: a wait with a limit is
+// followed by the vote, and one that ran out anywhere ends the loop everywhere.
+__device__ __forceinline__ void epilogue_sync() { asm volatile("barrier.cta.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ bool epilogue_agrees(bool yes) {
+  uint32_t all;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\tbarrier.cta.red.and.pred q, 1, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(all)
+      : "r"((uint32_t)yes)
+      : "memory");
+  return all != 0;
+}
+
+// The M operand from tensor memory.
+__device__ __forceinline__ void mma_f16(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add, uint32_t on) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add), "r"(on)
+      : "memory");
+}
+
+// 32 lanes x 32 columns: lane l of the warp writes tensor-memory lane
+// (warp % 4) * 32 + l.
+__device__ __forceinline__ void tmem_store32(uint32_t addr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),
+      "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+      "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(addr)
+      : "memory");
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// Four int8 -> two f16 pairs: the byte plus 128 becomes the low bits of a f16
+// of 1024 and more, from which 1024 + 128 is taken, exactly.
+__device__ __forceinline__ uint2 f16_of(uint32_t v) {
+  const uint32_t t = v ^ 0x80808080u;
+  uint2 r = make_uint2(__byte_perm(t, 0x64646464u, 0x4140), __byte_perm(t, 0x64646464u, 0x4342));
+  asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(r.x) : "r"(0x64806480u));
+  asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(r.y) : "r"(0x64806480u));
+  return r;
+}
+
+// Row tiles of an expert: as few as hold its rows, of equal width in steps of
+// 32; the last is as wide as what is left.
+__device__ __forceinline__ int tiles_of(int rows) { return (rows + kTileN - 1) / kTileN; }
+
+// A feature's gate is in the lane whose bit 3 is clear, its up eight lanes on.
+// Of the 32 rows that both hold, the lower lane gets gate and up of the even
+// ones, the upper lane those of the odd ones.
+__device__ __forceinline__ void pair_up(const float (&v)[32], bool upper, float (&g)[16], float (&u)[16]) {
 #pragma unroll
-      for (int c = 0; c < kWords; ++c)
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-#pragma unroll
-          for (int h = 0; h < kHalves; ++h) acc[h][i] = __dp4a(ws[h][f][c], xs[part * 8 + i][c], acc[h][i]);
-    }
-    if (f0 + f >= N) continue;
-    const float* sw = p.w_scales + (int64_t)e * kHalves * N + f0 + f;
-    for (int i = 0; i < 8; ++i) {
-      const int64_t r = r0 + part * 8 + i;
-      if (r >= hi) break;
-      const float sx = p.x_scales[r * p.x_scale_stride];
-      float v = __int2float_rn(acc[0][i]) * (sx * sw[0]);
-      if (GLU) v = swiglu_of(v, __int2float_rn(acc[kHalves - 1][i]) * (sx * sw[N]));
-      reinterpret_cast<uint16_t*>(p.out)[r * N + f0 + f] = (uint16_t)pack_bf16x2_rn(v, 0.0f);
-    }
+  for (int i = 0; i < 16; ++i) {
+    const float give = upper ? v[2 * i] : v[2 * i + 1], keep = upper ? v[2 * i + 1] : v[2 * i];
+    const float got = __shfl_xor_sync(0xffffffffu, give, 8);
+    g[i] = upper ? got : keep;
+    u[i] = upper ? keep : got;
   }
 }
 
 template <bool GLU>
+__global__ void __launch_bounds__(kThreads, 1) k_expert_i8(ExpertI8Params p, const __grid_constant__ Maps maps, uint64_t wait_ns) {
+  extern __shared__ uint8_t expert_raw[];
+  uint8_t* loads = reinterpret_cast<uint8_t*>(((uintptr_t)expert_raw + 1023) & ~(uintptr_t)1023);
+  uint8_t* steps_mem = loads + kLoads * kLoadBytes;
+  uint8_t* leaving = steps_mem + kSteps * kStepBytes;
+  Control& sm = *reinterpret_cast<Control*>(leaving + kChunkBytes);
+  int32_t* first = reinterpret_cast<int32_t*>(&sm + 1);  // row tiles before expert e
+  const int warp = threadIdx.x >> 5, lane = (int)lane_id();
+  const int E = p.num_experts, K = p.in_features, N = p.out_features;
+  const uint32_t rank = cluster_rank();
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kLoads; ++i) {
+      mbar_init(&sm.loaded[i], 2);  // this block's two producers (and their bytes)
+      mbar_init(&sm.used[i], 8);    // the warps that turn it into f16
+    }
+    for (int i = 0; i < kSteps; ++i) {
+      mbar_init(&sm.full[i], 16);  // at the even block: those of both blocks
+      mbar_init(&sm.empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sm.acc_full[i], 1);
+      mbar_init(&sm.acc_empty[i], 8);  // at the even block, from both
+    }
+    mbar_init_fence();
+  }
+  if (threadIdx.x >= 32 && threadIdx.x < 36)  // for the first copies
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<const CUtensorMap*>(&maps) + (threadIdx.x - 32)) : "memory");
+  __syncthreads();
+  // (both blocks run before either allocates: the allocation works in both)
+  cluster_sync();
+  if (warp == 1) tmem_alloc(&sm.tmem, kTmemColumns);
+  pdl_wait();
+  pdl_trigger();
+  auto rows_of = [&](int e, int& lo) {
+    lo = max(p.row_begin[e], 0);
+    return max((int)min((int64_t)max(p.row_end[e], 0), p.rows) - lo, 0);
+  };
+  if (warp == 0) {
+    int carry = 0;
+    for (int e0 = 0; e0 < E; e0 += 32) {
+      const int e = e0 + lane;
+      int lo;
+      const int n = e < E ? tiles_of(rows_of(e, lo)) : 0;
+      const int inc = warp_inclusive_scan(n);
+      if (e < E) first[e] = carry + inc - n;
+      carry += __shfl_sync(0xffffffffu, inc, 31);
+    }
+    if (lane == 0) first[E] = carry;
+  }
+  tmem_fence_before();
+  __syncthreads();
+  tmem_fence_after();
+  const uint32_t tmem = sm.tmem;
+
+  // Tiles in order: expert, then features, then rows; pairs take one each in
+  // turn, each second round in the other direction (as the bf16 products do).
+  const int turn = 2 * (pairs - pair) - 1;
+  const int tile_features = GLU ? kTileM / 2 : kTileM;
+  const int across = (N + tile_features - 1) / tile_features;
+  const int num_tiles = first[E] * across;
+  const int steps = (K + kStepK - 1) / kStepK;  // of every tile
+  // The t-th tile; o is this warp's tile before, or has e = -1.
+  auto find = [&](int t, Tile& o) {
+    const int before = o.e;
+    o.e = max(o.e, 0);
+    while (t >= first[o.e + 1] * across) ++o.e;
+    if (o.e != before) o.rows = rows_of(o.e, o.lo);
+    const int many = first[o.e + 1] - first[o.e];
+    const int i = t - first[o.e] * across;
+    o.f0 = i / many * tile_features;
+    const int width = ((o.rows + many - 1) / many + 31) / 32 * 32;
+    o.n0 = i % many * width;
+    o.n = min(width, (max(o.rows - o.n0, 0) + 31) / 32 * 32);
+  };
+  Tile o;
+  o.e = -1;
+  bool ok = true;
+
+  if (warp == 0 || warp == 2) {  // this block's features, and its rows, into shared memory
+    const bool second = warp == 2;
+    const uint32_t on = elect_one();
+    int st = 0;
+    uint32_t phase = 1;  // a fresh barrier's phase before the first counts as complete
+    int filled = 0;      // stages filled so far, up to kLoads
+    for (int t = pair, jump = turn; ok && t < num_tiles; t += jump, jump = 2 * pairs - jump) {
+      find(t, o);
+      if (o.n <= 0) continue;
+      const int half = o.n / 2;
+      // the boxes of this block's half: 16 << i rows each, the larger first
+      const int sizes = half / 16;  // 1 to 6
+      const uint32_t bytes = second ? (uint32_t)half * kLoadK : kBytesA;
+      const int big = 31 - __clz(sizes), small = sizes & ~(1 << big);
+      const CUtensorMap *map = &maps.b[big], *map2 = &maps.b[small ? 31 - __clz(small) : 0];
+      const int feature = o.f0 + (int)rank * kHalfM;
+      const int row = o.lo + o.n0 + (int)rank * half;
+      for (int k0 = 0; k0 < K; k0 += kLoadK) {
+        if (!warp_wait(&sm.used[st], phase, wait_ns)) {
+          ok = false;
+          break;
+        }
+        uint8_t* to = loads + st * kLoadBytes + (second ? kBytesA : 0);
+        const uint32_t bar = smem_u32(&sm.loaded[st]);
+        arrive_expect_at(bar, bytes, on);
+        if (second) {
+          tma_load_2d(to, map, k0, row, bar, on);
+          if (small) tma_load_2d(to + (16 << big) * kLoadK, map2, k0, row + (16 << big), bar, on);
+        } else if (GLU) {
+          // 8 features of gate, the same 8 of up, and so on
+          tma_load_5d(to, &maps.a, k0, 0, 0, o.f0 / 8 + (int)rank * 8, o.e, bar, on);
+        } else {
+          tma_load_3d(to, &maps.a, k0, feature, o.e, bar, on);
+        }
+        next_stage<kLoads>(st, phase);
+        filled = min(filled + 1, kLoads);
+      }
+    }
+    if (!ok && on) g_expert_i8_status = MOE_ERR_TIMEOUT;
+    // No copy may land after the block has exited, whoever gave up: wait for
+    // those of the stages filled last (two milliseconds at most each, where the
+    // other producer has not filled its part).
+    for (; filled > 0; --filled) {
+      if (st == 0) phase ^= 1u;
+      st = st == 0 ? kLoads - 1 : st - 1;
+      mbar_wait(&sm.loaded[st], phase ^ 1u, 2000000ull);
+    }
+  } else if (warp >= 4 && warp < 12) {  // 8 bits to f16: features (4-7), rows (8-11)
+    const bool second = warp >= 8;
+    const int quarter = warp & 3;
+    const uint32_t on = elect_one();
+    const uint32_t full0 = in_block(&sm.full[0], 0), used0 = smem_u32(&sm.used[0]);
+    int st = 0, cs = 0;
+    uint32_t phase = 0, step_phase = 1;
+    for (int t = pair, jump = turn; ok && t < num_tiles; t += jump, jump = 2 * pairs - jump) {
+      find(t, o);
+      if (o.n <= 0) continue;
+      const int groups = o.n / 16;  // of eight rows, in this block's half
+      for (int k = 0; k < steps; ++k) {
+        if ((k & 1) == 0 && !(ok = warp_wait(&sm.loaded[st], phase, wait_ns))) break;
+        if (!(ok = warp_wait(&sm.empty[cs], step_phase, wait_ns))) break;
+        const int c0 = (k & 1) * 4;  // the step's first 16-byte piece of a row's 128 bytes
+        const bool leave = (k & 1) || k == steps - 1;
+        if (!second) {
+          // lane = feature; its pieces lie where the swizzle put them
+          const uint8_t* from = loads + st * kLoadBytes + (quarter * 32 + lane) * kLoadK;
+          uint32_t r[32];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const uint4 v = *reinterpret_cast<const uint4*>(from + (((c0 + c) ^ (lane & 7)) << 4));
+            const uint2 a = f16_of(v.x), b = f16_of(v.y), d = f16_of(v.z), e = f16_of(v.w);
+            r[c * 8 + 0] = a.x, r[c * 8 + 1] = a.y, r[c * 8 + 2] = b.x, r[c * 8 + 3] = b.y;
+            r[c * 8 + 4] = d.x, r[c * 8 + 5] = d.y, r[c * 8 + 6] = e.x, r[c * 8 + 7] = e.y;
+          }
+          if (leave) {
+            __syncwarp();
+            arrive_local_at(used0 + 8u * st, on);
+          }
+          tmem_fence_after();  // the products that read the stage before are done
+          tmem_store32(tmem + (uint32_t)(quarter * 32) * 65536u + kFeatureColumn + cs * kStageColumns, r);
+          tmem_fence_before();
+          __syncwarp();
+          arrive_local_at(full0 + 8u * cs, on);
+        } else {
+          // eight rows x four pieces at a time, each piece to two of f16
+          const uint8_t* from = loads + st * kLoadBytes + kBytesA;
+          uint8_t* to = steps_mem + cs * kStepBytes;
+          const int r8 = lane & 7, c = lane >> 3;
+          for (int g = quarter; g < groups; g += 4) {
+            const int row = g * 8 + r8;
+            const uint4 v = *reinterpret_cast<const uint4*>(from + row * kLoadK + (((c0 + c) ^ r8) << 4));
+            const uint2 a = f16_of(v.x), b = f16_of(v.y), d = f16_of(v.z), e = f16_of(v.w);
+            *reinterpret_cast<uint4*>(to + row * 128 + (((2 * c) ^ r8) << 4)) = make_uint4(a.x, a.y, b.x, b.y);
+            *reinterpret_cast<uint4*>(to + row * 128 + (((2 * c + 1) ^ r8) << 4)) = make_uint4(d.x, d.y, e.x, e.y);
+          }
+          fence_proxy_async_smem();
+          if (leave) {
+            __syncwarp();
+            arrive_local_at(used0 + 8u * st, on);
+          }
+          arrive_with_shared_at(full0 + 8u * cs, on);
+        }
+        if (leave) next_stage<kLoads>(st, phase);
+        next_stage<kSteps>(cs, step_phase);
+      }
+    }
+    if (!ok && lane == 0) g_expert_i8_status = MOE_ERR_TIMEOUT;
+  } else if (warp == 1 && rank == 0) {  // tensor cores, for both blocks
+    int cs = 0, last = -1;  // last: the stage of the last MMAs, and its phase
+    uint32_t phase = 0, last_phase = 0;
+    const uint32_t on = elect_one();
+    int acc = 0;  // accumulators begun
+    for (int t = pair, jump = turn; ok && t < num_tiles; t += jump, jump = 2 * pairs - jump) {
+      find(t, o);
+      if (o.n <= 0) continue;
+      const int as = acc & 1;
+      if (acc >= 2 && !warp_wait(&sm.acc_empty[as], (uint32_t)((acc / 2 + 1) & 1), wait_ns)) {
+        ok = false;
+        break;
+      }
+      const uint32_t idesc = instr_desc(false, false, false, kTileM, o.n);
+      for (int k = 0; k < steps; ++k, next_stage<kSteps>(cs, phase)) {
+        if (!warp_wait_cluster(&sm.full[cs], phase, wait_ns)) {
+          ok = false;
+          break;
+        }
+        tmem_fence_after();
+        const uint64_t db = operand_desc(smem_u32(steps_mem + cs * kStepBytes), false);
+        const uint32_t a = tmem + kFeatureColumn + cs * kStageColumns;
+#pragma unroll
+        for (int i = 0; i < kStepK / 16; ++i)
+          mma_f16(tmem + as * kTileN, a + i * 8, db + i * 32 / 16, idesc, k > 0 || i > 0, on);
+        mma_commit(&sm.empty[cs], on);
+        if (k == steps - 1) mma_commit(&sm.acc_full[as], on);
+        last = cs;
+        last_phase = phase;
+      }
+      ++acc;
+    }
+    if (!ok && lane == 0) g_expert_i8_status = MOE_ERR_TIMEOUT;
+    // tensor memory is freed below: wait for the last MMAs, with the full budget
+    if (last >= 0) mbar_wait(&sm.empty[last], last_phase);
+  } else if (warp >= 12) {  // accumulators to memory: a warp reads tensor-memory lanes (warp % 4) * 32 ..
+    const int quarter = warp & 3, tid = (int)threadIdx.x - 12 * 32;
+    const uint32_t on = elect_one();
+    const uint32_t acc_empty0 = in_block(&sm.acc_empty[0], 0);
+    const bool upper = lane & 8;  // holds up
+    // this lane's feature of the block's
+    const int here = GLU ? quarter * 16 + (lane >> 4) * 8 + (lane & 7) : quarter * 32 + lane;
+    int acc = 0;
+    for (int t = pair, jump = turn; t < num_tiles; t += jump, jump = 2 * pairs - jump) {
+      find(t, o);
+      if (o.n <= 0) continue;
+      const int as = acc & 1;
+      const int own = GLU ? 64 : kHalfM;               // features of this block
+      const int f = o.f0 + (int)rank * own;
+      const int nf = min(max(N - f, 0), own);          // that exist, a multiple of 8
+      const int valid = min(o.n, o.rows - o.n0);       // rows of the tile that the expert has
+      const int64_t row0 = (int64_t)o.lo + o.n0;
+      // scales, while the products run: the lane's feature's, and the rows'
+      // (read behind the vote below)
+      float sw = 0.0f;
+      if (here < nf) sw = p.w_scales[(int64_t)o.e * (GLU ? 2 * N : N) + (GLU && upper ? N : 0) + f + here];
+      for (int i = tid; i < o.n; i += 128) sm.row_scales[as][i] = i < valid ? p.x_scales[(row0 + i) * p.x_scale_stride] : 0.0f;
+      ok = epilogue_agrees(warp_wait(&sm.acc_full[as], (uint32_t)((acc / 2) & 1), wait_ns));
+      if (!ok) break;
+      tmem_fence_after();
+      const uint32_t src = tmem + (uint32_t)(quarter * 32) * 65536u + (uint32_t)(as * kTileN);
+      for (int c = 0; c < o.n; c += kChunk) {
+        // features to rows through shared memory
+        float v[32];
+        tmem_load32(src + c, v);
+        if (c + kChunk >= o.n) {  // the last columns have been read: the accumulator is free
+          tmem_fence_before();
+          __syncwarp();
+          arrive_local_at(acc_empty0 + 8u * as, on);
+        }
+        const float4* sx = reinterpret_cast<const float4*>(sm.row_scales[as] + c);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float4 s = sx[i];
+          v[4 * i] *= s.x * sw;
+          v[4 * i + 1] *= s.y * sw;
+          v[4 * i + 2] *= s.z * sw;
+          v[4 * i + 3] *= s.w * sw;
+        }
+        if (c != 0) epilogue_sync();  // the rows before have been read (the tile's before: at the vote)
+        if (GLU) {
+          float g[16], u[16];
+          pair_up(v, upper, g, u);
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            reinterpret_cast<uint16_t*>(leaving + (2 * i + (upper ? 1 : 0)) * 256)[here] =
+                (uint16_t)pack_bf16x2_rn(swiglu_of(g[i], u[i]), 0.0f);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            reinterpret_cast<uint16_t*>(leaving + i * 256)[here] = (uint16_t)pack_bf16x2_rn(v[i], 0.0f);
+        }
+        epilogue_sync();
+        constexpr int kPieces = GLU ? 8 : 16;  // of eight features, in a row
+#pragma unroll
+        for (int j = 0; j < kChunk * kPieces / 128; ++j) {
+          const int i = j * 128 + tid, r = i / kPieces, at = i % kPieces * 8;
+          if (c + r < valid && at < nf)
+            st_v4(p.out + ((row0 + c + r) * N + f + at) * 2, *reinterpret_cast<const uint4*>(leaving + r * 256 + at * 2));
+        }
+      }
+      ++acc;
+    }
+    if (!ok && lane == 0) g_expert_i8_status = MOE_ERR_TIMEOUT;
+  }
+  __syncwarp();
+  tmem_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tmem_fence_after();
+  if (warp == 1) tmem_free(tmem, kTmemColumns);
+  __syncwarp();
+  cluster_sync();  // and neither leaves before both have freed theirs
+}
+
+// int8 in boxes of 128 bytes x `rows`; what lies outside reads as zero.
+bool make_map(CUtensorMap* map, const void* base, int dims, const cuuint64_t* size, const cuuint64_t* strides,
+              const cuuint32_t* box) {
+  const EncodeTiled fn = encode_tiled();
+  const cuuint32_t one[5] = {1, 1, 1, 1, 1};
+  return fn && fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, dims, const_cast<void*>(base), size, strides, box, one,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The pairs that can be resident at once on the current device, looked up once
+// per device and kernel.
+template <bool GLU>
+int resident_pairs(int dev, int sms) {
+  static std::once_flag once[64];
+  static int found[64];
+  if (dev >= 64) return 0;
+  std::call_once(once[dev], [&] {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(sms / 2 * 2));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem_bytes(MOE_MAX_EXPERTS);
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = 2;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, (const void*)k_expert_i8<GLU>, &cfg) != cudaSuccess) {
+      cudaGetLastError();
+      n = 0;
+    }
+    found[dev] = n;
+  });
+  return found[dev];
+}
+
+template <bool GLU>
 cudaError_t launch(const ExpertI8Params& p, cudaStream_t s) {
+  int dev = 0, sms = 0;
+  if (!current_device(&dev, &sms)) return cudaErrorInvalidDevice;
+  const cuuint64_t K = (cuuint64_t)p.in_features, N = (cuuint64_t)p.out_features, E = (cuuint64_t)p.num_experts;
+  Maps maps;
+  bool ok;
+  if (GLU) {
+    // w [E][2F][K] as [E][F / 8][gate, up][8][K], in boxes of 64 gate features,
+    // 8 by 8 in turn with their up features
+    const cuuint64_t size[5] = {K, 8, 2, N / 8, E}, strides[4] = {K, N * K, 8 * K, 2 * N * K};
+    const cuuint32_t box[5] = {kLoadK, 8, 2, 8, 1};
+    ok = make_map(&maps.a, p.w, 5, size, strides, box);
+  } else {
+    const cuuint64_t size[3] = {K, N, E}, strides[2] = {K, N * K};
+    const cuuint32_t box[3] = {kLoadK, kHalfM, 1};
+    ok = make_map(&maps.a, p.w, 3, size, strides, box);
+  }
+  for (int i = 0; i < 3; ++i) {
+    const cuuint64_t size[2] = {K, (cuuint64_t)p.rows}, strides[1] = {(cuuint64_t)p.x_stride};
+    const cuuint32_t box[2] = {kLoadK, 16u << i};
+    ok = ok && make_map(&maps.b[i], p.x, 2, size, strides, box);
+  }
+  if (!ok) return cudaErrorUnknown;
+  const void* fn = (const void*)k_expert_i8<GLU>;
+  cudaError_t err = ensure_dynamic_smem(fn, smem_bytes(MOE_MAX_EXPERTS));
+  if (err != cudaSuccess) return err;
+  const int64_t pairs = resident_pairs<GLU>(dev, sms);
+  if (pairs < 1) return cudaErrorInvalidConfiguration;
+  // the row counts are on the device: as many pairs as there can be tiles
+  const int64_t width = GLU ? kTileM / 2 : kTileM, across = (p.out_features + width - 1) / width;
+  const int64_t most = across * (p.num_experts + p.rows / kTileN);
   ExpertI8Params q = p;
-  void* args[] = {&q};
-  return launch_pdl((const void*)k_expert_i8<GLU>, dim3((unsigned)((p.out_features + kFeatures - 1) / kFeatures), (unsigned)p.num_experts),
-                    dim3(kThreads), 0, s, args);
+  uint64_t wait_ns = wait_limit_ns();
+  void* args[] = {&q, &maps, &wait_ns};
+  return launch_pdl(fn, dim3((unsigned)(2 * (most < pairs ? most : pairs))), dim3(kThreads), smem_bytes(p.num_experts), s,
+                    args, 2);
 }
 
 }  // namespace
+
+int read_expert_i8_status(int32_t* out, bool clear) {
+  int32_t v = 0;
+  const int32_t zero = MOE_OK;
+  if (cudaMemcpyFromSymbol(&v, g_expert_i8_status, 4) != cudaSuccess ||
+      (clear && cudaMemcpyToSymbol(g_expert_i8_status, &zero, 4) != cudaSuccess)) {
+    cudaGetLastError();
+    return MOE_ERR_CUDA;
+  }
+  *out = v;
+  return MOE_OK;
+}
 
 cudaError_t launch_expert_product_i8(const ExpertI8Params& p, cudaStream_t s) { return launch<false>(p, s); }
 cudaError_t launch_expert_swiglu_i8(const ExpertI8Params& p, cudaStream_t s) { return launch<true>(p, s); }

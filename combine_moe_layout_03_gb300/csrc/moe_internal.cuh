@@ -247,8 +247,9 @@ int read_device_status(int32_t* out, bool clear);
 // default kWaitLimitNs; clamped to it).
 void set_wait_limit_ns(uint64_t ns);
 uint64_t wait_limit_ns();
-// The experts' kernels' part of read_device_status.
+// The experts' kernels' part of read_device_status, and that of their 8-bit forms.
 int read_expert_status(int32_t* out, bool clear);
+int read_expert_i8_status(int32_t* out, bool clear);
 cudaError_t launch_slots(bool pack, const void* const* src, void* const* dst,
                          const moe_slot_desc_t* d, const int64_t* offsets, int64_t slot_bytes,
                          cudaStream_t s);

@@ -12,12 +12,14 @@
 // A pair of blocks (a cluster of two, tcgen05 cta_group::2) walks over output
 // tiles as the bf16 products do: 256 features (M), 128 to a block, by up to 192
 // rows of one expert (N), in steps of 32. Warps 0 and 2 load features and rows
-// with TMA, 128 reduction steps at a time. Warps 4-7 turn features into f16 and
+// with TMA, 128 reduction steps at a time. Warps 4-11 turn features into f16 and
 // put them into tensor memory, from where the products take their M operand:
 // shared memory, which is what a step is short of (it would read and write 96 KB
-// of it, 64 KB this way), then holds them in 8 bits only. Warps 8-11 turn rows into
-// f16 in shared memory. Warp 1 of the even block issues tcgen05.mma for both,
-// 64 reduction steps at a time; warps 12-15 scale what is finished and store it.
+// of it, 64 KB this way), then holds them in 8 bits only. Warps 12-19 turn rows
+// into f16 in shared memory. Both are two sets of four warps, which take one load
+// each in turn: a load's way through a set is longer than its products. Warp 1 of
+// the even block issues tcgen05.mma for both blocks; warps 20-23 scale what is
+// finished and store it.
 // Tensor memory holds two accumulators of 192 columns, so that a tile's
 // epilogue runs beside the next one's products, and four stages of features of
 // 32 columns.
@@ -32,13 +34,13 @@ namespace {
 constexpr int kTileM = 256, kTileN = 192;     // of a pair
 constexpr int kHalfM = 128;                   // of a block
 constexpr int kLoadK = 128, kStepK = 64;      // reduction steps loaded together, and multiplied together
-constexpr int kLoads = 5, kSteps = 4;         // stages of each
+constexpr int kLoads = 5, kSteps = 4;         // stages of each; a set's are two of the latter
 constexpr int kBytesA = kHalfM * kLoadK, kBytesB = kTileN / 2 * kLoadK, kLoadBytes = kBytesA + kBytesB;
 constexpr int kStepBytes = kTileN / 2 * kStepK * 2;  // rows as f16
 constexpr int kTmemColumns = 512;
 constexpr int kFeatureColumn = 2 * kTileN;    // of the first stage of features
 constexpr int kStageColumns = kStepK / 2;
-constexpr int kThreads = 512;
+constexpr int kThreads = 768;
 constexpr int kChunk = 32;                    // rows that leave together
 constexpr int kChunkBytes = kChunk * 256;     // 128 features in bf16
 
@@ -56,7 +58,7 @@ struct Tile {
 };
 
 struct Control {
-  uint64_t loaded[kLoads], used[kLoads], full[kSteps], empty[kSteps], acc_full[2], acc_empty[2];
+  uint64_t loaded[kLoads], used[kLoads], full[2], empty[kSteps], acc_full[2], acc_empty[2];
   uint32_t tmem;
   alignas(16) float row_scales[2][kTileN];  // read four at a time
 };
@@ -100,8 +102,8 @@ __device__ __forceinline__ void tmem_store32(uint32_t addr, const uint32_t (&r)[
       "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
       "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(addr)
       : "memory");
-  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
+__device__ __forceinline__ void tmem_store_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // Four int8 -> two f16 pairs: the byte plus 128 becomes the low bits of a f16
 // of 1024 and more, from which 1024 + 128 is taken, exactly.
@@ -146,13 +148,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_expert_i8(ExpertI8Params p, con
   if (threadIdx.x == 0) {
     for (int i = 0; i < kLoads; ++i) {
       mbar_init(&sm.loaded[i], 2);  // this block's two producers (and their bytes)
-      mbar_init(&sm.used[i], 8);    // the warps that turn it into f16
+      mbar_init(&sm.used[i], 8);    // the warps of a set
     }
-    for (int i = 0; i < kSteps; ++i) {
-      mbar_init(&sm.full[i], 16);  // at the even block: those of both blocks
-      mbar_init(&sm.empty[i], 1);
-    }
+    for (int i = 0; i < kSteps; ++i) mbar_init(&sm.empty[i], 1);
     for (int i = 0; i < 2; ++i) {
+      mbar_init(&sm.full[i], 16);  // at the even block: the set's warps of both blocks
       mbar_init(&sm.acc_full[i], 1);
       mbar_init(&sm.acc_empty[i], 8);  // at the even block, from both
     }
@@ -193,7 +193,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_expert_i8(ExpertI8Params p, con
   const int tile_features = GLU ? kTileM / 2 : kTileM;
   const int across = (N + tile_features - 1) / tile_features;
   const int num_tiles = first[E] * across;
-  const int steps = (K + kStepK - 1) / kStepK;  // of every tile
+  const int num_loads = (K + kLoadK - 1) / kLoadK;                                // of every tile
+  const bool short_end = K - (num_loads - 1) * kLoadK <= kStepK;                  // the last load is one step
   // The t-th tile; o is this warp's tile before, or has e = -1.
   auto find = [&](int t, Tile& o) {
     const int before = o.e;
@@ -258,68 +259,86 @@ __global__ void __launch_bounds__(kThreads, 1) k_expert_i8(ExpertI8Params p, con
       st = st == 0 ? kLoads - 1 : st - 1;
       mbar_wait(&sm.loaded[st], phase ^ 1u, 2000000ull);
     }
-  } else if (warp >= 4 && warp < 12) {  // 8 bits to f16: features (4-7), rows (8-11)
-    const bool second = warp >= 8;
-    const int quarter = warp & 3;
+  } else if (warp >= 4 && warp < 20) {  // 8 bits to f16: features (4-11), rows (12-19)
+    const bool second = warp >= 12;
+    const int quarter = warp & 3, set = ((warp - 4) >> 2) & 1;
     const uint32_t on = elect_one();
-    const uint32_t full0 = in_block(&sm.full[0], 0), used0 = smem_u32(&sm.used[0]);
-    int st = 0, cs = 0;
+    const uint32_t full = in_block(&sm.full[set], 0), used0 = smem_u32(&sm.used[0]);
+    const int r8 = lane & 7, piece = lane >> 3;
+    int st = 0, turn_of = 0;  // the set that the next load is for
     uint32_t phase = 0, step_phase = 1;
     for (int t = pair, jump = turn; ok && t < num_tiles; t += jump, jump = 2 * pairs - jump) {
       find(t, o);
       if (o.n <= 0) continue;
-      const int groups = o.n / 16;  // of eight rows, in this block's half
-      for (int k = 0; k < steps; ++k) {
-        if ((k & 1) == 0 && !(ok = warp_wait(&sm.loaded[st], phase, wait_ns))) break;
-        if (!(ok = warp_wait(&sm.empty[cs], step_phase, wait_ns))) break;
-        const int c0 = (k & 1) * 4;  // the step's first 16-byte piece of a row's 128 bytes
-        const bool leave = (k & 1) || k == steps - 1;
+      const int groups = o.n / 16;  // of eight rows, in this block's half: 2 to 12
+      for (int l = 0; l < num_loads; ++l, turn_of ^= 1, next_stage<kLoads>(st, phase)) {
+        if (turn_of != set) continue;
+        const int halves = short_end && l == num_loads - 1 ? 1 : 2;
+        if (!(ok = warp_wait(&sm.loaded[st], phase, wait_ns))) break;
+        const uint8_t* from = loads + st * kLoadBytes;
         if (!second) {
-          // lane = feature; its pieces lie where the swizzle put them
-          const uint8_t* from = loads + st * kLoadBytes + (quarter * 32 + lane) * kLoadK;
-          uint32_t r[32];
+          // lane = feature; its 16-byte pieces lie where the swizzle put them
+          uint4 v[8];
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const uint4 v = *reinterpret_cast<const uint4*>(from + (((c0 + c) ^ (lane & 7)) << 4));
-            const uint2 a = f16_of(v.x), b = f16_of(v.y), d = f16_of(v.z), e = f16_of(v.w);
-            r[c * 8 + 0] = a.x, r[c * 8 + 1] = a.y, r[c * 8 + 2] = b.x, r[c * 8 + 3] = b.y;
-            r[c * 8 + 4] = d.x, r[c * 8 + 5] = d.y, r[c * 8 + 6] = e.x, r[c * 8 + 7] = e.y;
+          for (int c = 0; c < 8; ++c)
+            v[c] = *reinterpret_cast<const uint4*>(from + (quarter * 32 + lane) * kLoadK + ((c ^ r8) << 4));
+          __syncwarp();
+          arrive_local_at(used0 + 8u * st, on);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (h == halves) break;
+            if (!(ok = warp_wait(&sm.empty[2 * set + h], step_phase, wait_ns))) break;
+            uint32_t r[32];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const uint2 a = f16_of(v[4 * h + c].x), b = f16_of(v[4 * h + c].y), d = f16_of(v[4 * h + c].z), e = f16_of(v[4 * h + c].w);
+              r[c * 8 + 0] = a.x, r[c * 8 + 1] = a.y, r[c * 8 + 2] = b.x, r[c * 8 + 3] = b.y;
+              r[c * 8 + 4] = d.x, r[c * 8 + 5] = d.y, r[c * 8 + 6] = e.x, r[c * 8 + 7] = e.y;
+            }
+            tmem_fence_after();  // the products that read the stage before are done
+            tmem_store32(tmem + (uint32_t)(quarter * 32) * 65536u + kFeatureColumn + (2 * set + h) * kStageColumns, r);
           }
-          if (leave) {
-            __syncwarp();
-            arrive_local_at(used0 + 8u * st, on);
-          }
-          tmem_fence_after();  // the products that read the stage before are done
-          tmem_store32(tmem + (uint32_t)(quarter * 32) * 65536u + kFeatureColumn + cs * kStageColumns, r);
+          if (!ok) break;
+          tmem_store_wait();
           tmem_fence_before();
           __syncwarp();
-          arrive_local_at(full0 + 8u * cs, on);
+          arrive_local_at(full, on);
         } else {
           // eight rows x four pieces at a time, each piece to two of f16
-          const uint8_t* from = loads + st * kLoadBytes + kBytesA;
-          uint8_t* to = steps_mem + cs * kStepBytes;
-          const int r8 = lane & 7, c = lane >> 3;
-          for (int g = quarter; g < groups; g += 4) {
-            const int row = g * 8 + r8;
-            const uint4 v = *reinterpret_cast<const uint4*>(from + row * kLoadK + (((c0 + c) ^ r8) << 4));
-            const uint2 a = f16_of(v.x), b = f16_of(v.y), d = f16_of(v.z), e = f16_of(v.w);
-            *reinterpret_cast<uint4*>(to + row * 128 + (((2 * c) ^ r8) << 4)) = make_uint4(a.x, a.y, b.x, b.y);
-            *reinterpret_cast<uint4*>(to + row * 128 + (((2 * c + 1) ^ r8) << 4)) = make_uint4(d.x, d.y, e.x, e.y);
+          from += kBytesA;
+          uint4 v[3][2];
+#pragma unroll
+          for (int i = 0; i < 3; ++i)
+            if (quarter + 4 * i < groups) {
+              const uint8_t* row = from + ((quarter + 4 * i) * 8 + r8) * kLoadK;
+#pragma unroll
+              for (int h = 0; h < 2; ++h) v[i][h] = *reinterpret_cast<const uint4*>(row + (((4 * h + piece) ^ r8) << 4));
+            }
+          __syncwarp();
+          arrive_local_at(used0 + 8u * st, on);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (h == halves) break;
+            if (!(ok = warp_wait(&sm.empty[2 * set + h], step_phase, wait_ns))) break;
+#pragma unroll
+            for (int i = 0; i < 3; ++i)
+              if (quarter + 4 * i < groups) {
+                uint8_t* to = steps_mem + (2 * set + h) * kStepBytes + ((quarter + 4 * i) * 8 + r8) * 128;
+                const uint2 a = f16_of(v[i][h].x), b = f16_of(v[i][h].y), d = f16_of(v[i][h].z), e = f16_of(v[i][h].w);
+                *reinterpret_cast<uint4*>(to + (((2 * piece) ^ r8) << 4)) = make_uint4(a.x, a.y, b.x, b.y);
+                *reinterpret_cast<uint4*>(to + (((2 * piece + 1) ^ r8) << 4)) = make_uint4(d.x, d.y, e.x, e.y);
+              }
           }
+          if (!ok) break;
           fence_proxy_async_smem();
-          if (leave) {
-            __syncwarp();
-            arrive_local_at(used0 + 8u * st, on);
-          }
-          arrive_with_shared_at(full0 + 8u * cs, on);
+          arrive_with_shared_at(full, on);
         }
-        if (leave) next_stage<kLoads>(st, phase);
-        next_stage<kSteps>(cs, step_phase);
+        step_phase ^= 1u;
       }
     }
     if (!ok && lane == 0) g_expert_i8_status = MOE_ERR_TIMEOUT;
   } else if (warp == 1 && rank == 0) {  // tensor cores, for both blocks
-    int cs = 0, last = -1;  // last: the stage of the last MMAs, and its phase
+    int set = 0, last = -1;  // last: the set of the last MMAs, and its phase
     uint32_t phase = 0, last_phase = 0;
     const uint32_t on = elect_one();
     int acc = 0;  // accumulators begun
@@ -332,29 +351,35 @@ __global__ void __launch_bounds__(kThreads, 1) k_expert_i8(ExpertI8Params p, con
         break;
       }
       const uint32_t idesc = instr_desc(false, false, false, kTileM, o.n);
-      for (int k = 0; k < steps; ++k, next_stage<kSteps>(cs, phase)) {
-        if (!warp_wait_cluster(&sm.full[cs], phase, wait_ns)) {
+      for (int l = 0; l < num_loads; ++l, next_stage<2>(set, phase)) {
+        if (!warp_wait_cluster(&sm.full[set], phase, wait_ns)) {
           ok = false;
           break;
         }
         tmem_fence_after();
-        const uint64_t db = operand_desc(smem_u32(steps_mem + cs * kStepBytes), false);
-        const uint32_t a = tmem + kFeatureColumn + cs * kStageColumns;
+        const bool end = l == num_loads - 1;
 #pragma unroll
-        for (int i = 0; i < kStepK / 16; ++i)
-          mma_f16(tmem + as * kTileN, a + i * 8, db + i * 32 / 16, idesc, k > 0 || i > 0, on);
-        mma_commit(&sm.empty[cs], on);
-        if (k == steps - 1) mma_commit(&sm.acc_full[as], on);
-        last = cs;
+        for (int h = 0; h < 2; ++h) {
+          if (!(h == 1 && end && short_end)) {
+            const uint64_t db = operand_desc(smem_u32(steps_mem + (2 * set + h) * kStepBytes), false);
+            const uint32_t a = tmem + kFeatureColumn + (2 * set + h) * kStageColumns;
+#pragma unroll
+            for (int i = 0; i < kStepK / 16; ++i)
+              mma_f16(tmem + as * kTileN, a + i * 8, db + i * 32 / 16, idesc, l > 0 || h > 0 || i > 0, on);
+          }
+          mma_commit(&sm.empty[2 * set + h], on);
+        }
+        if (end) mma_commit(&sm.acc_full[as], on);
+        last = set;
         last_phase = phase;
       }
       ++acc;
     }
     if (!ok && lane == 0) g_expert_i8_status = MOE_ERR_TIMEOUT;
     // tensor memory is freed below: wait for the last MMAs, with the full budget
-    if (last >= 0) mbar_wait(&sm.empty[last], last_phase);
-  } else if (warp >= 12) {  // accumulators to memory: a warp reads tensor-memory lanes (warp % 4) * 32 ..
-    const int quarter = warp & 3, tid = (int)threadIdx.x - 12 * 32;
+    if (last >= 0) mbar_wait(&sm.empty[2 * last + 1], last_phase);
+  } else if (warp >= 20) {  // accumulators to memory: a warp reads tensor-memory lanes (warp % 4) * 32 ..
+    const int quarter = warp & 3, tid = (int)threadIdx.x - 20 * 32;
     const uint32_t on = elect_one();
     const uint32_t acc_empty0 = in_block(&sm.acc_empty[0], 0);
     const bool upper = lane & 8;  // holds up

@@ -34,9 +34,9 @@ namespace {
 constexpr int kTileM = 256, kTileN = 192;     // of a pair
 constexpr int kHalfM = 128;                   // of a block
 constexpr int kLoadK = 128, kStepK = 64;      // reduction steps loaded together, and multiplied together
-constexpr int kLoads = 5, kSteps = 4;         // stages of each; a set's are two of the latter
+constexpr int kLoads = 4, kTmemLoads = 2;     // stages of what is loaded, and of features as f16
 constexpr int kBytesA = kHalfM * kLoadK, kBytesB = kTileN / 2 * kLoadK, kLoadBytes = kBytesA + kBytesB;
-constexpr int kStepBytes = kTileN / 2 * kStepK * 2;  // rows as f16
+constexpr int kRowBytes = kTileN / 2 * kLoadK * 2;  // a load's rows as f16: two steps, one behind the other
 constexpr int kTmemColumns = 512;
 constexpr int kFeatureColumn = 2 * kTileN;    // of the first stage of features
 constexpr int kStageColumns = kStepK / 2;
@@ -58,12 +58,13 @@ struct Tile {
 };
 
 struct Control {
-  uint64_t loaded[kLoads], used[kLoads], full[2], empty[kSteps], acc_full[2], acc_empty[2];
+  uint64_t loaded[kLoads], used[kLoads], acc_full[2], acc_empty[2];
+  uint64_t features[kTmemLoads], features_done[2 * kTmemLoads], rows[kLoads], rows_done[kLoads];
   uint32_t tmem;
   alignas(16) float row_scales[2][kTileN];  // read four at a time
 };
 constexpr size_t smem_bytes(int experts) {
-  return 1024 + (size_t)kLoads * kLoadBytes + (size_t)kSteps * kStepBytes + kChunkBytes + sizeof(Control) + ((size_t)experts + 1) * 4;
+  return 1024 + (size_t)kLoads * kLoadBytes + (size_t)kLoads * kRowBytes + kChunkBytes + sizeof(Control) + ((size_t)experts + 1) * 4;
 }
 
 // Named barrier of the epilogue warps, and a vote at it. It waits without a
@@ -105,14 +106,29 @@ __device__ __forceinline__ void tmem_store32(uint32_t addr, const uint32_t (&r)[
 }
 __device__ __forceinline__ void tmem_store_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void st_shared_v4(uint32_t addr, const uint32_t* r) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]) : "memory");
+}
+
 // Four int8 -> two f16 pairs: the byte plus 128 becomes the low bits of a f16
 // of 1024 and more, from which 1024 + 128 is taken, exactly.
-__device__ __forceinline__ uint2 f16_of(uint32_t v) {
+__device__ __forceinline__ void f16_of(uint32_t v, uint32_t* r) {
   const uint32_t t = v ^ 0x80808080u;
-  uint2 r = make_uint2(__byte_perm(t, 0x64646464u, 0x4140), __byte_perm(t, 0x64646464u, 0x4342));
-  asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(r.x) : "r"(0x64806480u));
-  asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(r.y) : "r"(0x64806480u));
-  return r;
+  r[0] = __byte_perm(t, 0x64646464u, 0x4140);
+  r[1] = __byte_perm(t, 0x64646464u, 0x4342);
+  asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(r[0]) : "r"(0x64806480u));
+  asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(r[1]) : "r"(0x64806480u));
+}
+__device__ __forceinline__ void f16_of(uint4 v, uint32_t* r) {
+  f16_of(v.x, r);
+  f16_of(v.y, r + 2);
+  f16_of(v.z, r + 4);
+  f16_of(v.w, r + 6);
 }
 
 // Row tiles of an expert: as few as hold its rows, of equal width in steps of
@@ -136,8 +152,8 @@ template <bool GLU>
 __global__ void __launch_bounds__(kThreads, 1) k_expert_i8(ExpertI8Params p, const __grid_constant__ Maps maps, uint64_t wait_ns) {
   extern __shared__ uint8_t expert_raw[];
   uint8_t* loads = reinterpret_cast<uint8_t*>(((uintptr_t)expert_raw + 1023) & ~(uintptr_t)1023);
-  uint8_t* steps_mem = loads + kLoads * kLoadBytes;
-  uint8_t* leaving = steps_mem + kSteps * kStepBytes;
+  uint8_t* rows_mem = loads + kLoads * kLoadBytes;
+  uint8_t* leaving = rows_mem + kLoads * kRowBytes;
   Control& sm = *reinterpret_cast<Control*>(leaving + kChunkBytes);
   int32_t* first = reinterpret_cast<int32_t*>(&sm + 1);  // row tiles before expert e
   const int warp = threadIdx.x >> 5, lane = (int)lane_id();
@@ -150,9 +166,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_expert_i8(ExpertI8Params p, con
       mbar_init(&sm.loaded[i], 2);  // this block's two producers (and their bytes)
       mbar_init(&sm.used[i], 8);    // the warps of a set
     }
-    for (int i = 0; i < kSteps; ++i) mbar_init(&sm.empty[i], 1);
+    // at the even block: a set's warps of both blocks
+    for (int i = 0; i < kTmemLoads; ++i) mbar_init(&sm.features[i], 8);
+    for (int i = 0; i < kLoads; ++i) mbar_init(&sm.rows[i], 8);
+    for (int i = 0; i < 2 * kTmemLoads; ++i) mbar_init(&sm.features_done[i], 1);
+    for (int i = 0; i < kLoads; ++i) mbar_init(&sm.rows_done[i], 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&sm.full[i], 16);  // at the even block: the set's warps of both blocks
       mbar_init(&sm.acc_full[i], 1);
       mbar_init(&sm.acc_empty[i], 8);  // at the even block, from both
     }
@@ -259,87 +278,78 @@ __global__ void __launch_bounds__(kThreads, 1) k_expert_i8(ExpertI8Params p, con
       st = st == 0 ? kLoads - 1 : st - 1;
       mbar_wait(&sm.loaded[st], phase ^ 1u, 2000000ull);
     }
-  } else if (warp >= 4 && warp < 20) {  // 8 bits to f16: features (4-11), rows (12-19)
-    const bool second = warp >= 12;
-    const int quarter = warp & 3, set = ((warp - 4) >> 2) & 1;
+  } else if (warp >= 4 && warp < 12) {  // features, 8 bits to f16
+    const int quarter = warp & 3, set = (warp - 4) >> 2;
     const uint32_t on = elect_one();
-    const uint32_t full = in_block(&sm.full[set], 0), used0 = smem_u32(&sm.used[0]);
-    const int r8 = lane & 7, piece = lane >> 3;
-    int st = 0, turn_of = 0;  // the set that the next load is for
-    uint32_t phase = 0, step_phase = 1;
+    const uint32_t features = in_block(&sm.features[set], 0);
+    const uint32_t to = tmem + (uint32_t)(quarter * 32) * 65536u + kFeatureColumn + 2 * set * kStageColumns;
+    // lane = feature; its 16-byte pieces lie where the swizzle put them
+    const uint32_t from0 = smem_u32(loads) + (uint32_t)((quarter * 32 + lane) * kLoadK + ((lane & 7) << 4));
+    uint32_t j = set, tiles_end = 0;  // this set's next load, the loads of all tiles so far
     for (int t = pair, jump = turn; ok && t < num_tiles; t += jump, jump = 2 * pairs - jump) {
       find(t, o);
       if (o.n <= 0) continue;
-      const int groups = o.n / 16;  // of eight rows, in this block's half: 2 to 12
-      for (int l = 0; l < num_loads; ++l, turn_of ^= 1, next_stage<kLoads>(st, phase)) {
-        if (turn_of != set) continue;
-        const int halves = short_end && l == num_loads - 1 ? 1 : 2;
-        if (!(ok = warp_wait(&sm.loaded[st], phase, wait_ns))) break;
-        const uint8_t* from = loads + st * kLoadBytes;
-        if (!second) {
-          // lane = feature; its 16-byte pieces lie where the swizzle put them
-          uint4 v[8];
+      for (tiles_end += num_loads; j < tiles_end; j += 2) {
+        const uint32_t st = j % kLoads, phase = (j / 2 + 1) & 1;
+        if (!(ok = warp_wait(&sm.loaded[st], (j / kLoads) & 1, wait_ns))) break;
+        const uint32_t from = from0 + st * kLoadBytes;
+        // (behind a last load of one step are zeros, which nothing multiplies)
 #pragma unroll
-          for (int c = 0; c < 8; ++c)
-            v[c] = *reinterpret_cast<const uint4*>(from + (quarter * 32 + lane) * kLoadK + ((c ^ r8) << 4));
-          __syncwarp();
-          arrive_local_at(used0 + 8u * st, on);
+        for (int h = 0; h < 2; ++h) {
+          uint32_t r[32];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            if (h == halves) break;
-            if (!(ok = warp_wait(&sm.empty[2 * set + h], step_phase, wait_ns))) break;
-            uint32_t r[32];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              const uint2 a = f16_of(v[4 * h + c].x), b = f16_of(v[4 * h + c].y), d = f16_of(v[4 * h + c].z), e = f16_of(v[4 * h + c].w);
-              r[c * 8 + 0] = a.x, r[c * 8 + 1] = a.y, r[c * 8 + 2] = b.x, r[c * 8 + 3] = b.y;
-              r[c * 8 + 4] = d.x, r[c * 8 + 5] = d.y, r[c * 8 + 6] = e.x, r[c * 8 + 7] = e.y;
-            }
-            tmem_fence_after();  // the products that read the stage before are done
-            tmem_store32(tmem + (uint32_t)(quarter * 32) * 65536u + kFeatureColumn + (2 * set + h) * kStageColumns, r);
-          }
-          if (!ok) break;
-          tmem_store_wait();
-          tmem_fence_before();
-          __syncwarp();
-          arrive_local_at(full, on);
-        } else {
-          // eight rows x four pieces at a time, each piece to two of f16
-          from += kBytesA;
-          uint4 v[3][2];
-#pragma unroll
-          for (int i = 0; i < 3; ++i)
-            if (quarter + 4 * i < groups) {
-              const uint8_t* row = from + ((quarter + 4 * i) * 8 + r8) * kLoadK;
-#pragma unroll
-              for (int h = 0; h < 2; ++h) v[i][h] = *reinterpret_cast<const uint4*>(row + (((4 * h + piece) ^ r8) << 4));
-            }
-          __syncwarp();
-          arrive_local_at(used0 + 8u * st, on);
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            if (h == halves) break;
-            if (!(ok = warp_wait(&sm.empty[2 * set + h], step_phase, wait_ns))) break;
-#pragma unroll
-            for (int i = 0; i < 3; ++i)
-              if (quarter + 4 * i < groups) {
-                uint8_t* to = steps_mem + (2 * set + h) * kStepBytes + ((quarter + 4 * i) * 8 + r8) * 128;
-                const uint2 a = f16_of(v[i][h].x), b = f16_of(v[i][h].y), d = f16_of(v[i][h].z), e = f16_of(v[i][h].w);
-                *reinterpret_cast<uint4*>(to + (((2 * piece) ^ r8) << 4)) = make_uint4(a.x, a.y, b.x, b.y);
-                *reinterpret_cast<uint4*>(to + (((2 * piece + 1) ^ r8) << 4)) = make_uint4(d.x, d.y, e.x, e.y);
-              }
-          }
-          if (!ok) break;
-          fence_proxy_async_smem();
-          arrive_with_shared_at(full, on);
+          for (int c = 0; c < 4; ++c) f16_of(ld_shared_v4(from ^ ((4 * h + c) << 4)), r + 8 * c);
+          if (!(ok = warp_wait(&sm.features_done[2 * set + h], phase, wait_ns))) break;
+          tmem_fence_after();  // the products that read the stage before are done
+          tmem_store32(to + h * kStageColumns, r);
         }
-        step_phase ^= 1u;
+        if (!ok) break;
+        tmem_store_wait();
+        tmem_fence_before();
+        __syncwarp();
+        arrive_local_at(features, on);
+        if (on) mbar_arrive(&sm.used[st]);
+      }
+    }
+    if (!ok && lane == 0) g_expert_i8_status = MOE_ERR_TIMEOUT;
+  } else if (warp >= 12 && warp < 20) {  // rows, 8 bits to f16
+    const int quarter = warp & 3, set = (warp - 12) >> 2;
+    const uint32_t on = elect_one();
+    const uint32_t rows0 = in_block(&sm.rows[0], 0);
+    // eight rows x four pieces of a step at a time, each piece to two of f16
+    const uint32_t r8 = lane & 7, piece = lane >> 3, row = quarter * 8 + r8;
+    const uint32_t from0 = smem_u32(loads) + kBytesA + row * kLoadK + ((piece ^ r8) << 4);
+    const uint32_t to0 = smem_u32(rows_mem) + row * 128 + (((2 * piece) ^ r8) << 4);
+    uint32_t j = set, tiles_end = 0;
+    for (int t = pair, jump = turn; ok && t < num_tiles; t += jump, jump = 2 * pairs - jump) {
+      find(t, o);
+      if (o.n <= 0) continue;
+      const int groups = o.n / 16 - quarter;  // of eight rows, each fourth of them this warp's
+      for (tiles_end += num_loads; j < tiles_end; j += 2) {
+        const uint32_t st = j % kLoads, phase = (j / kLoads) & 1;
+        if (!(ok = warp_wait(&sm.loaded[st], phase, wait_ns))) break;
+        if (!(ok = warp_wait(&sm.rows_done[st], phase ^ 1, wait_ns))) break;
+        const uint32_t from = from0 + st * kLoadBytes, to = to0 + st * kRowBytes;
+#pragma unroll
+        for (int i = 0; i < 3; ++i)
+          if (4 * i < groups) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              uint32_t r[8];
+              f16_of(ld_shared_v4((from + i * 32 * kLoadK) ^ (h << 6)), r);
+              const uint32_t at = to + h * (kRowBytes / 2) + i * 32 * 128;
+              st_shared_v4(at, r);
+              st_shared_v4(at ^ 16, r + 4);
+            }
+          }
+        fence_proxy_async_smem();
+        arrive_with_shared_at(rows0 + 8u * st, on);
+        if (on) mbar_arrive(&sm.used[st]);
       }
     }
     if (!ok && lane == 0) g_expert_i8_status = MOE_ERR_TIMEOUT;
   } else if (warp == 1 && rank == 0) {  // tensor cores, for both blocks
-    int set = 0, last = -1;  // last: the set of the last MMAs, and its phase
-    uint32_t phase = 0, last_phase = 0;
+    uint32_t j = 0;  // loads multiplied
     const uint32_t on = elect_one();
     int acc = 0;  // accumulators begun
     for (int t = pair, jump = turn; ok && t < num_tiles; t += jump, jump = 2 * pairs - jump) {
@@ -351,8 +361,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_expert_i8(ExpertI8Params p, con
         break;
       }
       const uint32_t idesc = instr_desc(false, false, false, kTileM, o.n);
-      for (int l = 0; l < num_loads; ++l, next_stage<2>(set, phase)) {
-        if (!warp_wait_cluster(&sm.full[set], phase, wait_ns)) {
+      for (int l = 0; l < num_loads; ++l, ++j) {
+        const uint32_t st = j % kLoads, fs = j % kTmemLoads;
+        if (!warp_wait_cluster(&sm.rows[st], (j / kLoads) & 1, wait_ns) ||
+            !warp_wait(&sm.features[fs], (j / kTmemLoads) & 1, wait_ns)) {
           ok = false;
           break;
         }
@@ -361,23 +373,22 @@ __global__ void __launch_bounds__(kThreads, 1) k_expert_i8(ExpertI8Params p, con
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           if (!(h == 1 && end && short_end)) {
-            const uint64_t db = operand_desc(smem_u32(steps_mem + (2 * set + h) * kStepBytes), false);
-            const uint32_t a = tmem + kFeatureColumn + (2 * set + h) * kStageColumns;
+            const uint64_t db = operand_desc(smem_u32(rows_mem + st * kRowBytes + h * (kRowBytes / 2)), false);
+            const uint32_t a = tmem + kFeatureColumn + (2 * fs + h) * kStageColumns;
 #pragma unroll
             for (int i = 0; i < kStepK / 16; ++i)
               mma_f16(tmem + as * kTileN, a + i * 8, db + i * 32 / 16, idesc, l > 0 || h > 0 || i > 0, on);
           }
-          mma_commit(&sm.empty[2 * set + h], on);
+          mma_commit(&sm.features_done[2 * fs + h], on);
         }
+        mma_commit(&sm.rows_done[st], on);
         if (end) mma_commit(&sm.acc_full[as], on);
-        last = set;
-        last_phase = phase;
       }
       ++acc;
     }
     if (!ok && lane == 0) g_expert_i8_status = MOE_ERR_TIMEOUT;
     // tensor memory is freed below: wait for the last MMAs, with the full budget
-    if (last >= 0) mbar_wait(&sm.empty[2 * last + 1], last_phase);
+    if (j > 0) mbar_wait(&sm.rows_done[(j - 1) % kLoads], ((j - 1) / kLoads) & 1);
   } else if (warp >= 20) {  // accumulators to memory: a warp reads tensor-memory lanes (warp % 4) * 32 ..
     const int quarter = warp & 3, tid = (int)threadIdx.x - 20 * 32;
     const uint32_t on = elect_one();

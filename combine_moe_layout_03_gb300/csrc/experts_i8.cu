@@ -34,12 +34,12 @@ namespace {
 constexpr int kTileM = 256, kTileN = 192;     // of a pair
 constexpr int kHalfM = 128;                   // of a block
 constexpr int kLoadK = 128, kStepK = 64;      // reduction steps loaded together, and multiplied together
-constexpr int kLoads = 4, kTmemLoads = 2;     // stages of what is loaded, and of features as f16
+constexpr int kLoads = 4;                     // stages of what is loaded, and of rows as f16
+constexpr int kMostFeatures = 7, kDone = 8;   // of features as f16 at most, and of what is multiplied
 constexpr int kBytesA = kHalfM * kLoadK, kBytesB = kTileN / 2 * kLoadK, kLoadBytes = kBytesA + kBytesB;
 constexpr int kRowBytes = kTileN / 2 * kLoadK * 2;  // a load's rows as f16: two steps, one behind the other
 constexpr int kTmemColumns = 512;
-constexpr int kFeatureColumn = 2 * kTileN;    // of the first stage of features
-constexpr int kStageColumns = kStepK / 2;
+constexpr int kStageColumns = kLoadK / 2;     // a load's features as f16
 constexpr int kThreads = 768;
 constexpr int kChunk = 32;                    // rows that leave together
 constexpr int kChunkBytes = kChunk * 256;     // 128 features in bf16
@@ -59,8 +59,9 @@ struct Tile {
 
 struct Control {
   uint64_t loaded[kLoads], used[kLoads], acc_full[2], acc_empty[2];
-  uint64_t features[kTmemLoads], features_done[2 * kTmemLoads], rows[kLoads], rows_done[kLoads];
+  uint64_t features[kMostFeatures], rows[kLoads], done[kDone];
   uint32_t tmem;
+  int32_t width;  // of the widest tile
   alignas(16) float row_scales[2][kTileN];  // read four at a time
 };
 constexpr size_t smem_bytes(int experts) {
@@ -134,6 +135,7 @@ __device__ __forceinline__ void f16_of(uint4 v, uint32_t* r) {
 // Row tiles of an expert: as few as hold its rows, of equal width in steps of
 // 32; the last is as wide as what is left.
 __device__ __forceinline__ int tiles_of(int rows) { return (rows + kTileN - 1) / kTileN; }
+__device__ __forceinline__ int width_of(int rows, int tiles) { return ((rows + tiles - 1) / tiles + 31) / 32 * 32; }
 
 // A feature's gate is in the lane whose bit 3 is clear, its up eight lanes on.
 // Of the 32 rows that both hold, the lower lane gets gate and up of the even
@@ -148,15 +150,21 @@ __device__ __forceinline__ void pair_up(const float (&v)[32], bool upper, float 
   }
 }
 
+// What all lanes of a warp hold alike, in a form that tells the compiler so:
+// it then keeps it, and what follows from it, in uniform registers, where the
+// operands of copies and products have to be.
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+
 template <bool GLU>
 __global__ void __launch_bounds__(kThreads, 1) k_expert_i8(ExpertI8Params p, const __grid_constant__ Maps maps, uint64_t wait_ns) {
   extern __shared__ uint8_t expert_raw[];
-  uint8_t* loads = reinterpret_cast<uint8_t*>(((uintptr_t)expert_raw + 1023) & ~(uintptr_t)1023);
+  // (an offset, so that the compiler knows these for addresses of shared memory)
+  uint8_t* loads = expert_raw + (-smem_u32(expert_raw) & 1023u);
   uint8_t* rows_mem = loads + kLoads * kLoadBytes;
   uint8_t* leaving = rows_mem + kLoads * kRowBytes;
   Control& sm = *reinterpret_cast<Control*>(leaving + kChunkBytes);
   int32_t* first = reinterpret_cast<int32_t*>(&sm + 1);  // row tiles before expert e
-  const int warp = threadIdx.x >> 5, lane = (int)lane_id();
+  const int warp = uniform(threadIdx.x >> 5), lane = (int)lane_id();
   const int E = p.num_experts, K = p.in_features, N = p.out_features;
   const uint32_t rank = cluster_rank();
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
@@ -167,10 +175,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_expert_i8(ExpertI8Params p, con
       mbar_init(&sm.used[i], 8);    // the warps of a set
     }
     // at the even block: a set's warps of both blocks
-    for (int i = 0; i < kTmemLoads; ++i) mbar_init(&sm.features[i], 8);
+    for (int i = 0; i < kMostFeatures; ++i) mbar_init(&sm.features[i], 8);
     for (int i = 0; i < kLoads; ++i) mbar_init(&sm.rows[i], 8);
-    for (int i = 0; i < 2 * kTmemLoads; ++i) mbar_init(&sm.features_done[i], 1);
-    for (int i = 0; i < kLoads; ++i) mbar_init(&sm.rows_done[i], 1);
+    for (int i = 0; i < kDone; ++i) mbar_init(&sm.done[i], 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.acc_full[i], 1);
       mbar_init(&sm.acc_empty[i], 8);  // at the even block, from both
@@ -190,40 +197,53 @@ __global__ void __launch_bounds__(kThreads, 1) k_expert_i8(ExpertI8Params p, con
     return max((int)min((int64_t)max(p.row_end[e], 0), p.rows) - lo, 0);
   };
   if (warp == 0) {
-    int carry = 0;
+    int carry = 0, width = 32;
     for (int e0 = 0; e0 < E; e0 += 32) {
       const int e = e0 + lane;
       int lo;
-      const int n = e < E ? tiles_of(rows_of(e, lo)) : 0;
+      const int rows = e < E ? rows_of(e, lo) : 0, n = tiles_of(rows);
+      if (n > 0) width = max(width, width_of(rows, n));
       const int inc = warp_inclusive_scan(n);
       if (e < E) first[e] = carry + inc - n;
       carry += __shfl_sync(0xffffffffu, inc, 31);
     }
-    if (lane == 0) first[E] = carry;
+    width = __reduce_max_sync(0xffffffffu, width);
+    if (lane == 0) {
+      first[E] = carry;
+      sm.width = width;
+    }
   }
   tmem_fence_before();
   __syncthreads();
   tmem_fence_after();
-  const uint32_t tmem = sm.tmem;
+  const uint32_t tmem = (uint32_t)uniform((int)sm.tmem);
+  // Tensor memory: two accumulators as wide as the widest tile, and in the rest
+  // as many stages of features as there is room for, 2 (192 rows) to 7 (32).
+  const uint32_t acc_columns = (uint32_t)uniform(sm.width), stages = (kTmemColumns - 2 * acc_columns) / kStageColumns;
+  const uint32_t tmem_features = tmem + 2 * acc_columns;
 
   // Tiles in order: expert, then features, then rows; pairs take one each in
   // turn, each second round in the other direction (as the bf16 products do).
   const int turn = 2 * (pairs - pair) - 1;
   const int tile_features = GLU ? kTileM / 2 : kTileM;
   const int across = (N + tile_features - 1) / tile_features;
-  const int num_tiles = first[E] * across;
+  const int num_tiles = uniform(first[E]) * across;
   const int num_loads = (K + kLoadK - 1) / kLoadK;                                // of every tile
   const bool short_end = K - (num_loads - 1) * kLoadK <= kStepK;                  // the last load is one step
   // The t-th tile; o is this warp's tile before, or has e = -1.
   auto find = [&](int t, Tile& o) {
     const int before = o.e;
     o.e = max(o.e, 0);
-    while (t >= first[o.e + 1] * across) ++o.e;
-    if (o.e != before) o.rows = rows_of(o.e, o.lo);
-    const int many = first[o.e + 1] - first[o.e];
-    const int i = t - first[o.e] * across;
+    while (t >= uniform(first[o.e + 1]) * across) ++o.e;
+    if (o.e != before) {
+      int lo;
+      o.rows = uniform(rows_of(o.e, lo));
+      o.lo = uniform(lo);
+    }
+    const int begin = uniform(first[o.e]), many = uniform(first[o.e + 1]) - begin;
+    const int i = t - begin * across;
     o.f0 = i / many * tile_features;
-    const int width = ((o.rows + many - 1) / many + 31) / 32 * 32;
+    const int width = width_of(o.rows, many);
     o.n0 = i % many * width;
     o.n = min(width, (max(o.rows - o.n0, 0) + 31) / 32 * 32);
   };
@@ -281,34 +301,34 @@ __global__ void __launch_bounds__(kThreads, 1) k_expert_i8(ExpertI8Params p, con
   } else if (warp >= 4 && warp < 12) {  // features, 8 bits to f16
     const int quarter = warp & 3, set = (warp - 4) >> 2;
     const uint32_t on = elect_one();
-    const uint32_t features = in_block(&sm.features[set], 0);
-    const uint32_t to = tmem + (uint32_t)(quarter * 32) * 65536u + kFeatureColumn + 2 * set * kStageColumns;
+    const uint32_t features0 = in_block(&sm.features[0], 0);
+    const uint32_t to = tmem_features + (uint32_t)(quarter * 32) * 65536u;
     // lane = feature; its 16-byte pieces lie where the swizzle put them
     const uint32_t from0 = smem_u32(loads) + (uint32_t)((quarter * 32 + lane) * kLoadK + ((lane & 7) << 4));
     uint32_t j = set, tiles_end = 0;  // this set's next load, the loads of all tiles so far
+    uint32_t fs = set;                // its stage of features
     for (int t = pair, jump = turn; ok && t < num_tiles; t += jump, jump = 2 * pairs - jump) {
       find(t, o);
       if (o.n <= 0) continue;
       for (tiles_end += num_loads; j < tiles_end; j += 2) {
-        const uint32_t st = j % kLoads, phase = (j / 2 + 1) & 1;
+        const uint32_t st = j % kLoads, before = j - stages;  // the load that had the stage of features
         if (!(ok = warp_wait(&sm.loaded[st], (j / kLoads) & 1, wait_ns))) break;
         const uint32_t from = from0 + st * kLoadBytes;
+        uint32_t r[2][32];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) f16_of(ld_shared_v4(from ^ (c << 4)), r[c / 4] + c % 4 * 8);
+        __syncwarp();
+        if (on) mbar_arrive(&sm.used[st]);
+        if (j >= stages && !(ok = warp_wait(&sm.done[before % kDone], (before / kDone) & 1, wait_ns))) break;
+        tmem_fence_after();  // the products that read the stage are done
         // (behind a last load of one step are zeros, which nothing multiplies)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t r[32];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) f16_of(ld_shared_v4(from ^ ((4 * h + c) << 4)), r + 8 * c);
-          if (!(ok = warp_wait(&sm.features_done[2 * set + h], phase, wait_ns))) break;
-          tmem_fence_after();  // the products that read the stage before are done
-          tmem_store32(to + h * kStageColumns, r);
-        }
-        if (!ok) break;
+        for (int h = 0; h < 2; ++h) tmem_store32(to + fs * kStageColumns + h * (kStageColumns / 2), r[h]);
         tmem_store_wait();
         tmem_fence_before();
         __syncwarp();
-        arrive_local_at(features, on);
-        if (on) mbar_arrive(&sm.used[st]);
+        arrive_local_at(features0 + 8u * fs, on);
+        if ((fs += 2) >= stages) fs -= stages;
       }
     }
     if (!ok && lane == 0) g_expert_i8_status = MOE_ERR_TIMEOUT;
@@ -326,9 +346,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_expert_i8(ExpertI8Params p, con
       if (o.n <= 0) continue;
       const int groups = o.n / 16 - quarter;  // of eight rows, each fourth of them this warp's
       for (tiles_end += num_loads; j < tiles_end; j += 2) {
-        const uint32_t st = j % kLoads, phase = (j / kLoads) & 1;
-        if (!(ok = warp_wait(&sm.loaded[st], phase, wait_ns))) break;
-        if (!(ok = warp_wait(&sm.rows_done[st], phase ^ 1, wait_ns))) break;
+        const uint32_t st = j % kLoads, before = j - kLoads;  // the load that had the stage of rows
+        if (!(ok = warp_wait(&sm.loaded[st], (j / kLoads) & 1, wait_ns))) break;
+        if (j >= kLoads && !(ok = warp_wait(&sm.done[before % kDone], (before / kDone) & 1, wait_ns))) break;
         const uint32_t from = from0 + st * kLoadBytes, to = to0 + st * kRowBytes;
 #pragma unroll
         for (int i = 0; i < 3; ++i)
@@ -349,7 +369,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_expert_i8(ExpertI8Params p, con
     }
     if (!ok && lane == 0) g_expert_i8_status = MOE_ERR_TIMEOUT;
   } else if (warp == 1 && rank == 0) {  // tensor cores, for both blocks
-    uint32_t j = 0;  // loads multiplied
+    uint32_t j = 0;               // loads multiplied
+    uint32_t fs = 0, phase = 0;   // stage of features
     const uint32_t on = elect_one();
     int acc = 0;  // accumulators begun
     for (int t = pair, jump = turn; ok && t < num_tiles; t += jump, jump = 2 * pairs - jump) {
@@ -362,9 +383,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_expert_i8(ExpertI8Params p, con
       }
       const uint32_t idesc = instr_desc(false, false, false, kTileM, o.n);
       for (int l = 0; l < num_loads; ++l, ++j) {
-        const uint32_t st = j % kLoads, fs = j % kTmemLoads;
-        if (!warp_wait_cluster(&sm.rows[st], (j / kLoads) & 1, wait_ns) ||
-            !warp_wait(&sm.features[fs], (j / kTmemLoads) & 1, wait_ns)) {
+        const uint32_t st = j % kLoads;
+        if (!warp_wait_cluster(&sm.rows[st], (j / kLoads) & 1, wait_ns) || !warp_wait(&sm.features[fs], phase, wait_ns)) {
           ok = false;
           break;
         }
@@ -372,23 +392,25 @@ __global__ void __launch_bounds__(kThreads, 1) k_expert_i8(ExpertI8Params p, con
         const bool end = l == num_loads - 1;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          if (!(h == 1 && end && short_end)) {
-            const uint64_t db = operand_desc(smem_u32(rows_mem + st * kRowBytes + h * (kRowBytes / 2)), false);
-            const uint32_t a = tmem + kFeatureColumn + (2 * fs + h) * kStageColumns;
+          if (h == 1 && end && short_end) break;
+          const uint64_t db = operand_desc(smem_u32(rows_mem + st * kRowBytes + h * (kRowBytes / 2)), false);
+          const uint32_t a = tmem_features + fs * kStageColumns + h * (kStageColumns / 2);
 #pragma unroll
-            for (int i = 0; i < kStepK / 16; ++i)
-              mma_f16(tmem + as * kTileN, a + i * 8, db + i * 32 / 16, idesc, l > 0 || h > 0 || i > 0, on);
-          }
-          mma_commit(&sm.features_done[2 * fs + h], on);
+          for (int i = 0; i < kStepK / 16; ++i)
+            mma_f16(tmem + as * acc_columns, a + i * 8, db + i * 32 / 16, idesc, l > 0 || h > 0 || i > 0, on);
         }
-        mma_commit(&sm.rows_done[st], on);
+        mma_commit(&sm.done[j % kDone], on);
         if (end) mma_commit(&sm.acc_full[as], on);
+        if (++fs == stages) {
+          fs = 0;
+          phase ^= 1u;
+        }
       }
       ++acc;
     }
     if (!ok && lane == 0) g_expert_i8_status = MOE_ERR_TIMEOUT;
     // tensor memory is freed below: wait for the last MMAs, with the full budget
-    if (j > 0) mbar_wait(&sm.rows_done[(j - 1) % kLoads], ((j - 1) / kLoads) & 1);
+    if (j > 0) mbar_wait(&sm.done[(j - 1) % kDone], ((j - 1) / kDone) & 1);
   } else if (warp >= 20) {  // accumulators to memory: a warp reads tensor-memory lanes (warp % 4) * 32 ..
     const int quarter = warp & 3, tid = (int)threadIdx.x - 20 * 32;
     const uint32_t on = elect_one();
@@ -414,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_expert_i8(ExpertI8Params p, con
       ok = epilogue_agrees(warp_wait(&sm.acc_full[as], (uint32_t)((acc / 2) & 1), wait_ns));
       if (!ok) break;
       tmem_fence_after();
-      const uint32_t src = tmem + (uint32_t)(quarter * 32) * 65536u + (uint32_t)(as * kTileN);
+      const uint32_t src = tmem + (uint32_t)(quarter * 32) * 65536u + as * acc_columns;
       for (int c = 0; c < o.n; c += kChunk) {
         // features to rows through shared memory
         float v[32];

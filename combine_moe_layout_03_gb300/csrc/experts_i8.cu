@@ -34,10 +34,12 @@ namespace {
 constexpr int kTileM = 256, kTileN = 192;     // of a pair
 constexpr int kHalfM = 128;                   // of a block
 constexpr int kLoadK = 128, kStepK = 64;      // reduction steps loaded together, and multiplied together
-constexpr int kLoads = 4;                     // stages of what is loaded, and of rows as f16
-constexpr int kMostFeatures = 7, kDone = 8;   // of features as f16 at most, and of what is multiplied
-constexpr int kBytesA = kHalfM * kLoadK, kBytesB = kTileN / 2 * kLoadK, kLoadBytes = kBytesA + kBytesB;
-constexpr int kRowBytes = kTileN / 2 * kLoadK * 2;  // a load's rows as f16: two steps, one behind the other
+// Stages: of what is loaded (4 to 10, by the widest tile), of features as f16
+// (2 to 7), of rows as f16, and of barriers between converters and products,
+// which are more than stages of either.
+constexpr int kMostLoads = 10, kRowStages = 4, kRing = 8;
+constexpr int kBytesA = kHalfM * kLoadK;
+constexpr int kStageBytes = 4 * (kBytesA + kTileN / 2 * kLoadK) + kRowStages * kTileN * kLoadK;  // for all of them
 constexpr int kTmemColumns = 512;
 constexpr int kStageColumns = kLoadK / 2;     // a load's features as f16
 constexpr int kThreads = 768;
@@ -58,14 +60,14 @@ struct Tile {
 };
 
 struct Control {
-  uint64_t loaded[kLoads], used[kLoads], acc_full[2], acc_empty[2];
-  uint64_t features[kMostFeatures], rows[kLoads], done[kDone];
+  uint64_t loaded[kMostLoads], used[kMostLoads], acc_full[2], acc_empty[2];
+  uint64_t full[kRing], done[kRing];
   uint32_t tmem;
   int32_t width;  // of the widest tile
   alignas(16) float row_scales[2][kTileN];  // read four at a time
 };
 constexpr size_t smem_bytes(int experts) {
-  return 1024 + (size_t)kLoads * kLoadBytes + (size_t)kLoads * kRowBytes + kChunkBytes + sizeof(Control) + ((size_t)experts + 1) * 4;
+  return 1024 + (size_t)kStageBytes + kChunkBytes + sizeof(Control) + ((size_t)experts + 1) * 4;
 }
 
 // Named barrier of the epilogue warps, and a vote at it. It waits without a
@@ -160,8 +162,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_expert_i8(ExpertI8Params p, con
   extern __shared__ uint8_t expert_raw[];
   // (an offset, so that the compiler knows these for addresses of shared memory)
   uint8_t* loads = expert_raw + (-smem_u32(expert_raw) & 1023u);
-  uint8_t* rows_mem = loads + kLoads * kLoadBytes;
-  uint8_t* leaving = rows_mem + kLoads * kRowBytes;
+  uint8_t* leaving = loads + kStageBytes;
   Control& sm = *reinterpret_cast<Control*>(leaving + kChunkBytes);
   int32_t* first = reinterpret_cast<int32_t*>(&sm + 1);  // row tiles before expert e
   const int warp = uniform(threadIdx.x >> 5), lane = (int)lane_id();
@@ -170,14 +171,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_expert_i8(ExpertI8Params p, con
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kLoads; ++i) {
+    for (int i = 0; i < kMostLoads; ++i) {
       mbar_init(&sm.loaded[i], 2);  // this block's two producers (and their bytes)
       mbar_init(&sm.used[i], 8);    // the warps of a set
     }
-    // at the even block: a set's warps of both blocks
-    for (int i = 0; i < kMostFeatures; ++i) mbar_init(&sm.features[i], 8);
-    for (int i = 0; i < kLoads; ++i) mbar_init(&sm.rows[i], 8);
-    for (int i = 0; i < kDone; ++i) mbar_init(&sm.done[i], 1);
+    for (int i = 0; i < kRing; ++i) {
+      mbar_init(&sm.full[i], 16);  // at the even block: a set's warps of both blocks
+      mbar_init(&sm.done[i], 1);
+    }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.acc_full[i], 1);
       mbar_init(&sm.acc_empty[i], 8);  // at the even block, from both
@@ -220,6 +221,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_expert_i8(ExpertI8Params p, con
   // Tensor memory: two accumulators as wide as the widest tile, and in the rest
   // as many stages of features as there is room for, 2 (192 rows) to 7 (32).
   const uint32_t acc_columns = (uint32_t)uniform(sm.width), stages = (kTmemColumns - 2 * acc_columns) / kStageColumns;
+  // Shared memory: stages of rows for that width, and in the rest as many loads
+  // as there is room for: the fewer rows, the more weights are under way.
+  const uint32_t row_bytes = acc_columns * kLoadK;  // a load's rows as f16: two steps, one behind the other
+  const uint32_t load_bytes = kBytesA + acc_columns / 2 * kLoadK;
+  const uint32_t num_stages = min((kStageBytes - kRowStages * row_bytes) / load_bytes, (uint32_t)kMostLoads);
+  const uint32_t loads_mem = smem_u32(loads), rows_mem = loads_mem + num_stages * load_bytes;
   const uint32_t tmem_features = tmem + 2 * acc_columns;
 
   // Tiles in order: expert, then features, then rows; pairs take one each in
@@ -254,9 +261,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_expert_i8(ExpertI8Params p, con
   if (warp == 0 || warp == 2) {  // this block's features, and its rows, into shared memory
     const bool second = warp == 2;
     const uint32_t on = elect_one();
-    int st = 0;
-    uint32_t phase = 1;  // a fresh barrier's phase before the first counts as complete
-    int filled = 0;      // stages filled so far, up to kLoads
+    uint32_t st = 0, phase = 1;  // a fresh barrier's phase before the first counts as complete
+    uint32_t filled = 0;         // stages filled so far, up to all
     for (int t = pair, jump = turn; ok && t < num_tiles; t += jump, jump = 2 * pairs - jump) {
       find(t, o);
       if (o.n <= 0) continue;
@@ -273,7 +279,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_expert_i8(ExpertI8Params p, con
           ok = false;
           break;
         }
-        uint8_t* to = loads + st * kLoadBytes + (second ? kBytesA : 0);
+        uint8_t* to = loads + st * load_bytes + (second ? kBytesA : 0);
         const uint32_t bar = smem_u32(&sm.loaded[st]);
         arrive_expect_at(bar, bytes, on);
         if (second) {
@@ -285,8 +291,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_expert_i8(ExpertI8Params p, con
         } else {
           tma_load_3d(to, &maps.a, k0, feature, o.e, bar, on);
         }
-        next_stage<kLoads>(st, phase);
-        filled = min(filled + 1, kLoads);
+        if (++st == num_stages) {
+          st = 0;
+          phase ^= 1u;
+        }
+        filled = min(filled + 1, num_stages);
       }
     }
     if (!ok && on) g_expert_i8_status = MOE_ERR_TIMEOUT;
@@ -295,31 +304,36 @@ __global__ void __launch_bounds__(kThreads, 1) k_expert_i8(ExpertI8Params p, con
     // other producer has not filled its part).
     for (; filled > 0; --filled) {
       if (st == 0) phase ^= 1u;
-      st = st == 0 ? kLoads - 1 : st - 1;
+      st = st == 0 ? num_stages - 1 : st - 1;
       mbar_wait(&sm.loaded[st], phase ^ 1u, 2000000ull);
     }
   } else if (warp >= 4 && warp < 12) {  // features, 8 bits to f16
     const int quarter = warp & 3, set = (warp - 4) >> 2;
     const uint32_t on = elect_one();
-    const uint32_t features0 = in_block(&sm.features[0], 0);
+    const uint32_t full0 = in_block(&sm.full[0], 0);
     const uint32_t to = tmem_features + (uint32_t)(quarter * 32) * 65536u;
     // lane = feature; its 16-byte pieces lie where the swizzle put them
-    const uint32_t from0 = smem_u32(loads) + (uint32_t)((quarter * 32 + lane) * kLoadK + ((lane & 7) << 4));
+    const uint32_t from0 = loads_mem + (uint32_t)((quarter * 32 + lane) * kLoadK + ((lane & 7) << 4));
     uint32_t j = set, tiles_end = 0;  // this set's next load, the loads of all tiles so far
     uint32_t fs = set;                // its stage of features
+    uint32_t st = set, phase = 0;     // and of what is loaded
     for (int t = pair, jump = turn; ok && t < num_tiles; t += jump, jump = 2 * pairs - jump) {
       find(t, o);
       if (o.n <= 0) continue;
       for (tiles_end += num_loads; j < tiles_end; j += 2) {
-        const uint32_t st = j % kLoads, before = j - stages;  // the load that had the stage of features
-        if (!(ok = warp_wait(&sm.loaded[st], (j / kLoads) & 1, wait_ns))) break;
-        const uint32_t from = from0 + st * kLoadBytes;
+        const uint32_t before = j - stages;  // the load that had the stage of features
+        if (!(ok = warp_wait(&sm.loaded[st], phase, wait_ns))) break;
+        const uint32_t from = from0 + st * load_bytes;
         uint32_t r[2][32];
 #pragma unroll
         for (int c = 0; c < 8; ++c) f16_of(ld_shared_v4(from ^ (c << 4)), r[c / 4] + c % 4 * 8);
         __syncwarp();
         if (on) mbar_arrive(&sm.used[st]);
-        if (j >= stages && !(ok = warp_wait(&sm.done[before % kDone], (before / kDone) & 1, wait_ns))) break;
+        if ((st += 2) >= num_stages) {
+          st -= num_stages;
+          phase ^= 1u;
+        }
+        if (j >= stages && !(ok = warp_wait(&sm.done[before % kRing], (before / kRing) & 1, wait_ns))) break;
         tmem_fence_after();  // the products that read the stage are done
         // (behind a last load of one step are zeros, which nothing multiplies)
 #pragma unroll
@@ -327,7 +341,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_expert_i8(ExpertI8Params p, con
         tmem_store_wait();
         tmem_fence_before();
         __syncwarp();
-        arrive_local_at(features0 + 8u * fs, on);
+        arrive_local_at(full0 + 8u * (j % kRing), on);
         if ((fs += 2) >= stages) fs -= stages;
       }
     }
@@ -335,42 +349,55 @@ __global__ void __launch_bounds__(kThreads, 1) k_expert_i8(ExpertI8Params p, con
   } else if (warp >= 12 && warp < 20) {  // rows, 8 bits to f16
     const int quarter = warp & 3, set = (warp - 12) >> 2;
     const uint32_t on = elect_one();
-    const uint32_t rows0 = in_block(&sm.rows[0], 0);
+    const uint32_t full0 = in_block(&sm.full[0], 0);
     // eight rows x four pieces of a step at a time, each piece to two of f16
     const uint32_t r8 = lane & 7, piece = lane >> 3, row = quarter * 8 + r8;
-    const uint32_t from0 = smem_u32(loads) + kBytesA + row * kLoadK + ((piece ^ r8) << 4);
-    const uint32_t to0 = smem_u32(rows_mem) + row * 128 + (((2 * piece) ^ r8) << 4);
+    const uint32_t from0 = loads_mem + kBytesA + row * kLoadK + ((piece ^ r8) << 4);
+    const uint32_t to0 = rows_mem + row * 128 + (((2 * piece) ^ r8) << 4);
     uint32_t j = set, tiles_end = 0;
+    uint32_t st = set, phase = 0;
     for (int t = pair, jump = turn; ok && t < num_tiles; t += jump, jump = 2 * pairs - jump) {
       find(t, o);
       if (o.n <= 0) continue;
       const int groups = o.n / 16 - quarter;  // of eight rows, each fourth of them this warp's
       for (tiles_end += num_loads; j < tiles_end; j += 2) {
-        const uint32_t st = j % kLoads, before = j - kLoads;  // the load that had the stage of rows
-        if (!(ok = warp_wait(&sm.loaded[st], (j / kLoads) & 1, wait_ns))) break;
-        if (j >= kLoads && !(ok = warp_wait(&sm.done[before % kDone], (before / kDone) & 1, wait_ns))) break;
-        const uint32_t from = from0 + st * kLoadBytes, to = to0 + st * kRowBytes;
+        const uint32_t before = j - kRowStages;  // the load that had the stage of rows
+        if (!(ok = warp_wait(&sm.loaded[st], phase, wait_ns))) break;
+        const uint32_t from = from0 + st * load_bytes, to = to0 + j % kRowStages * row_bytes;
+        uint4 v[3][2];
+#pragma unroll
+        for (int i = 0; i < 3; ++i)
+          if (4 * i < groups) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) v[i][h] = ld_shared_v4((from + i * 32 * kLoadK) ^ (h << 6));
+          }
+        __syncwarp();
+        if (on) mbar_arrive(&sm.used[st]);
+        if ((st += 2) >= num_stages) {
+          st -= num_stages;
+          phase ^= 1u;
+        }
+        if (j >= kRowStages && !(ok = warp_wait(&sm.done[before % kRing], (before / kRing) & 1, wait_ns))) break;
 #pragma unroll
         for (int i = 0; i < 3; ++i)
           if (4 * i < groups) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               uint32_t r[8];
-              f16_of(ld_shared_v4((from + i * 32 * kLoadK) ^ (h << 6)), r);
-              const uint32_t at = to + h * (kRowBytes / 2) + i * 32 * 128;
+              f16_of(v[i][h], r);
+              const uint32_t at = to + h * (row_bytes / 2) + i * 32 * 128;
               st_shared_v4(at, r);
               st_shared_v4(at ^ 16, r + 4);
             }
           }
         fence_proxy_async_smem();
-        arrive_with_shared_at(rows0 + 8u * st, on);
-        if (on) mbar_arrive(&sm.used[st]);
+        arrive_with_shared_at(full0 + 8u * (j % kRing), on);
       }
     }
     if (!ok && lane == 0) g_expert_i8_status = MOE_ERR_TIMEOUT;
   } else if (warp == 1 && rank == 0) {  // tensor cores, for both blocks
     uint32_t j = 0;               // loads multiplied
-    uint32_t fs = 0, phase = 0;   // stage of features
+    uint32_t fs = 0;              // stage of features
     const uint32_t on = elect_one();
     int acc = 0;  // accumulators begun
     for (int t = pair, jump = turn; ok && t < num_tiles; t += jump, jump = 2 * pairs - jump) {
@@ -383,34 +410,27 @@ __global__ void __launch_bounds__(kThreads, 1) k_expert_i8(ExpertI8Params p, con
       }
       const uint32_t idesc = instr_desc(false, false, false, kTileM, o.n);
       for (int l = 0; l < num_loads; ++l, ++j) {
-        const uint32_t st = j % kLoads;
-        if (!warp_wait_cluster(&sm.rows[st], (j / kLoads) & 1, wait_ns) || !warp_wait(&sm.features[fs], phase, wait_ns)) {
-          ok = false;
-          break;
-        }
+        if (!(ok = warp_wait_cluster(&sm.full[j % kRing], (j / kRing) & 1, wait_ns))) break;
         tmem_fence_after();
         const bool end = l == num_loads - 1;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           if (h == 1 && end && short_end) break;
-          const uint64_t db = operand_desc(smem_u32(rows_mem + st * kRowBytes + h * (kRowBytes / 2)), false);
+          const uint64_t db = operand_desc(rows_mem + j % kRowStages * row_bytes + h * (row_bytes / 2), false);
           const uint32_t a = tmem_features + fs * kStageColumns + h * (kStageColumns / 2);
 #pragma unroll
           for (int i = 0; i < kStepK / 16; ++i)
             mma_f16(tmem + as * acc_columns, a + i * 8, db + i * 32 / 16, idesc, l > 0 || h > 0 || i > 0, on);
         }
-        mma_commit(&sm.done[j % kDone], on);
+        mma_commit(&sm.done[j % kRing], on);
         if (end) mma_commit(&sm.acc_full[as], on);
-        if (++fs == stages) {
-          fs = 0;
-          phase ^= 1u;
-        }
+        if (++fs == stages) fs = 0;
       }
       ++acc;
     }
     if (!ok && lane == 0) g_expert_i8_status = MOE_ERR_TIMEOUT;
     // tensor memory is freed below: wait for the last MMAs, with the full budget
-    if (j > 0) mbar_wait(&sm.done[(j - 1) % kDone], ((j - 1) / kDone) & 1);
+    if (j > 0) mbar_wait(&sm.done[(j - 1) % kRing], ((j - 1) / kRing) & 1);
   } else if (warp >= 20) {  // accumulators to memory: a warp reads tensor-memory lanes (warp % 4) * 32 ..
     const int quarter = warp & 3, tid = (int)threadIdx.x - 20 * 32;
     const uint32_t on = elect_one();

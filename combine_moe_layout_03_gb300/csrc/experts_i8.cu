@@ -85,11 +85,44 @@ __device__ __forceinline__ bool epilogue_agrees(bool yes) {
   return all != 0;
 }
 
-// The M operand from tensor memory.
-__device__ __forceinline__ void mma_f16(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add, uint32_t on) {
+// A wait of a whole warp: all lanes ask at once and go on together, without a
+// branch that the compiler would have to expect them to take apart.
+template <bool CLUSTER>
+__device__ __forceinline__ bool asks(uint64_t* bar, uint32_t parity) {
+  if (!CLUSTER) return __all_sync(0xffffffffu, mbar_try_wait(bar, parity));
+  uint32_t ok;
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-      "@q tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return __all_sync(0xffffffffu, ok);
+}
+template <bool CLUSTER = false>
+__device__ __forceinline__ bool waits(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
+  if (limit_ns < kWaitLimitNs)  // a lowered budget (test hook): polls without suspending
+    return CLUSTER ? warp_wait_cluster(bar, parity, limit_ns) : warp_wait(bar, parity, limit_ns);
+  if (asks<CLUSTER>(bar, parity)) return true;
+  const uint64_t t0 = global_timer_ns();
+  while (!asks<CLUSTER>(bar, parity)) {
+    if (__any_sync(0xffffffffu, global_timer_ns() - t0 > limit_ns)) return false;
+  }
+  return true;
+}
+
+// One step's products, the M operand from tensor memory: four of 16 reduction
+// steps each, which are 8 columns of it and 32 bytes of the rows.
+__device__ __forceinline__ void mma_step(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add, uint32_t on) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .b32 a1, a2, a3;\n\t.reg .b64 b1, b2, b3;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "add.u32 a1, %1, 8;\n\tadd.u32 a2, %1, 16;\n\tadd.u32 a3, %1, 24;\n\t"
+      "add.u64 b1, %2, 2;\n\tadd.u64 b2, %2, 4;\n\tadd.u64 b3, %2, 6;\n\t"
+      "@q tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+      "@q tcgen05.mma.cta_group::2.kind::f16 [%0], [a1], b1, %3, 1;\n\t"
+      "@q tcgen05.mma.cta_group::2.kind::f16 [%0], [a2], b2, %3, 1;\n\t"
+      "@q tcgen05.mma.cta_group::2.kind::f16 [%0], [a3], b3, %3, 1;\n\t}" ::"r"(d),
       "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add), "r"(on)
       : "memory");
 }
@@ -275,7 +308,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_expert_i8(ExpertI8Params p, con
       const int feature = o.f0 + (int)rank * kHalfM;
       const int row = o.lo + o.n0 + (int)rank * half;
       for (int k0 = 0; k0 < K; k0 += kLoadK) {
-        if (!warp_wait(&sm.used[st], phase, wait_ns)) {
+        if (!waits(&sm.used[st], phase, wait_ns)) {
           ok = false;
           break;
         }
@@ -322,7 +355,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_expert_i8(ExpertI8Params p, con
       if (o.n <= 0) continue;
       for (tiles_end += num_loads; j < tiles_end; j += 2) {
         const uint32_t before = j - stages;  // the load that had the stage of features
-        if (!(ok = warp_wait(&sm.loaded[st], phase, wait_ns))) break;
+        if (!(ok = waits(&sm.loaded[st], phase, wait_ns))) break;
         const uint32_t from = from0 + st * load_bytes;
         uint32_t r[2][32];
 #pragma unroll
@@ -333,7 +366,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_expert_i8(ExpertI8Params p, con
           st -= num_stages;
           phase ^= 1u;
         }
-        if (j >= stages && !(ok = warp_wait(&sm.done[before % kRing], (before / kRing) & 1, wait_ns))) break;
+        if (j >= stages && !(ok = waits(&sm.done[before % kRing], (before / kRing) & 1, wait_ns))) break;
         tmem_fence_after();  // the products that read the stage are done
         // (behind a last load of one step are zeros, which nothing multiplies)
 #pragma unroll
@@ -362,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_expert_i8(ExpertI8Params p, con
       const int groups = o.n / 16 - quarter;  // of eight rows, each fourth of them this warp's
       for (tiles_end += num_loads; j < tiles_end; j += 2) {
         const uint32_t before = j - kRowStages;  // the load that had the stage of rows
-        if (!(ok = warp_wait(&sm.loaded[st], phase, wait_ns))) break;
+        if (!(ok = waits(&sm.loaded[st], phase, wait_ns))) break;
         const uint32_t from = from0 + st * load_bytes, to = to0 + j % kRowStages * row_bytes;
         uint4 v[3][2];
 #pragma unroll
@@ -377,7 +410,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_expert_i8(ExpertI8Params p, con
           st -= num_stages;
           phase ^= 1u;
         }
-        if (j >= kRowStages && !(ok = warp_wait(&sm.done[before % kRing], (before / kRing) & 1, wait_ns))) break;
+        if (j >= kRowStages && !(ok = waits(&sm.done[before % kRing], (before / kRing) & 1, wait_ns))) break;
 #pragma unroll
         for (int i = 0; i < 3; ++i)
           if (4 * i < groups) {
@@ -404,13 +437,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_expert_i8(ExpertI8Params p, con
       find(t, o);
       if (o.n <= 0) continue;
       const int as = acc & 1;
-      if (acc >= 2 && !warp_wait(&sm.acc_empty[as], (uint32_t)((acc / 2 + 1) & 1), wait_ns)) {
+      if (acc >= 2 && !waits(&sm.acc_empty[as], (uint32_t)((acc / 2 + 1) & 1), wait_ns)) {
         ok = false;
         break;
       }
       const uint32_t idesc = instr_desc(false, false, false, kTileM, o.n);
       for (int l = 0; l < num_loads; ++l, ++j) {
-        if (!(ok = warp_wait_cluster(&sm.full[j % kRing], (j / kRing) & 1, wait_ns))) break;
+        if (!(ok = waits<true>(&sm.full[j % kRing], (j / kRing) & 1, wait_ns))) break;
         tmem_fence_after();
         const bool end = l == num_loads - 1;
 #pragma unroll
@@ -418,9 +451,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_expert_i8(ExpertI8Params p, con
           if (h == 1 && end && short_end) break;
           const uint64_t db = operand_desc(rows_mem + j % kRowStages * row_bytes + h * (row_bytes / 2), false);
           const uint32_t a = tmem_features + fs * kStageColumns + h * (kStageColumns / 2);
-#pragma unroll
-          for (int i = 0; i < kStepK / 16; ++i)
-            mma_f16(tmem + as * acc_columns, a + i * 8, db + i * 32 / 16, idesc, l > 0 || h > 0 || i > 0, on);
+          mma_step(tmem + as * acc_columns, a, db, idesc, l > 0 || h > 0, on);
         }
         mma_commit(&sm.done[j % kRing], on);
         if (end) mma_commit(&sm.acc_full[as], on);
@@ -453,7 +484,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_expert_i8(ExpertI8Params p, con
       float sw = 0.0f;
       if (here < nf) sw = p.w_scales[(int64_t)o.e * (GLU ? 2 * N : N) + (GLU && upper ? N : 0) + f + here];
       for (int i = tid; i < o.n; i += 128) sm.row_scales[as][i] = i < valid ? p.x_scales[(row0 + i) * p.x_scale_stride] : 0.0f;
-      ok = epilogue_agrees(warp_wait(&sm.acc_full[as], (uint32_t)((acc / 2) & 1), wait_ns));
+      ok = epilogue_agrees(waits(&sm.acc_full[as], (uint32_t)((acc / 2) & 1), wait_ns));
       if (!ok) break;
       tmem_fence_after();
       const uint32_t src = tmem + (uint32_t)(quarter * 32) * 65536u + as * acc_columns;

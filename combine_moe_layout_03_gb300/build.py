@@ -20,7 +20,7 @@ LIB = os.path.join(PKG, "libmoe.so")
 OBJDIR = os.path.join(PKG, "_build")
 SOURCES = ["moe_api.cu", "layout.cu", "dispatch.cu", "combine.cu", "layout_static.cu",
            "slots.cu", "ranks.cu", "backward.cu", "layer_api.cu", "route.cu",
-           "swiglu.cu", "experts.cu", "quantize.cu", "experts_i8.cu"]
+           "swiglu.cu", "experts.cu", "quantize.cu", "experts_i8.cu", "experts_i8_few.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-I", INCLUDE]

@@ -619,6 +619,13 @@ cudaError_t launch(const ExpertI8Params& p, cudaStream_t s) {
                     args, 2);
 }
 
+// A few rows go to a kernel that streams the weights, if there are no more than
+// two for each expert on average: it takes two at a time and reads the weights
+// again for more, and tiles take the same time for 1 to 32. (First product 7168
+// -> 2 x 2048, here / there: 1 row 25 / 9 us, 8 rows in 8 experts 48 / 37, 16 in
+// 16 86 / 72, in 8 48 / 37, in one 24 / 87; 32 in 32 145 / 134, in 8 48 / 70.)
+bool few(const ExpertI8Params& p) { return p.rows <= kFewRows && p.rows <= 2 * (int64_t)p.num_experts; }
+
 }  // namespace
 
 int read_expert_i8_status(int32_t* out, bool clear) {
@@ -633,7 +640,11 @@ int read_expert_i8_status(int32_t* out, bool clear) {
   return MOE_OK;
 }
 
-cudaError_t launch_expert_product_i8(const ExpertI8Params& p, cudaStream_t s) { return launch<false>(p, s); }
-cudaError_t launch_expert_swiglu_i8(const ExpertI8Params& p, cudaStream_t s) { return launch<true>(p, s); }
+cudaError_t launch_expert_product_i8(const ExpertI8Params& p, cudaStream_t s) {
+  return few(p) ? launch_expert_i8_few(p, false, s) : launch<false>(p, s);
+}
+cudaError_t launch_expert_swiglu_i8(const ExpertI8Params& p, cudaStream_t s) {
+  return few(p) ? launch_expert_i8_few(p, true, s) : launch<true>(p, s);
+}
 
 }  // namespace moe

@@ -285,6 +285,9 @@ cudaError_t launch_expert_grad_weight(const ExpertParams& p, cudaStream_t s);
 cudaError_t launch_quantize(const QuantParams& p, cudaStream_t s);
 cudaError_t launch_expert_product_i8(const ExpertI8Params& p, cudaStream_t s);
 cudaError_t launch_expert_swiglu_i8(const ExpertI8Params& p, cudaStream_t s);
+// Either of the two for a few rows, at most kFewRows.
+constexpr int kFewRows = 16;
+cudaError_t launch_expert_i8_few(const ExpertI8Params& p, bool glu, cudaStream_t s);
 
 #ifdef __CUDACC__
 

@@ -357,20 +357,25 @@ __global__ void __launch_bounds__(kThreads, 1) k_expert_i8(ExpertI8Params p, con
         const uint32_t before = j - stages;  // the load that had the stage of features
         if (!(ok = waits(&sm.loaded[st], phase, wait_ns))) break;
         const uint32_t from = from0 + st * load_bytes;
-        uint32_t r[2][32];
+        // (behind a last load of one step are zeros, which nothing multiplies)
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+          uint32_t r[32];
 #pragma unroll
-        for (int c = 0; c < 8; ++c) f16_of(ld_shared_v4(from ^ (c << 4)), r[c / 4] + c % 4 * 8);
+          for (int c = 0; c < 4; ++c) f16_of(ld_shared_v4(from ^ (uint32_t)(h * 64 + c * 16)), r + c * 8);
+          if (h == 0) {
+            if (j >= stages && !(ok = waits(&sm.done[before % kRing], (before / kRing) & 1, wait_ns))) break;
+            tmem_fence_after();  // the products that read the stage are done
+          }
+          tmem_store32(to + fs * kStageColumns + h * (kStageColumns / 2), r);
+        }
+        if (!ok) break;
         __syncwarp();
         if (on) mbar_arrive(&sm.used[st]);
         if ((st += 2) >= num_stages) {
           st -= num_stages;
           phase ^= 1u;
         }
-        if (j >= stages && !(ok = waits(&sm.done[before % kRing], (before / kRing) & 1, wait_ns))) break;
-        tmem_fence_after();  // the products that read the stage are done
-        // (behind a last load of one step are zeros, which nothing multiplies)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) tmem_store32(to + fs * kStageColumns + h * (kStageColumns / 2), r[h]);
         tmem_store_wait();
         tmem_fence_before();
         __syncwarp();
@@ -397,32 +402,24 @@ __global__ void __launch_bounds__(kThreads, 1) k_expert_i8(ExpertI8Params p, con
         const uint32_t before = j - kRowStages;  // the load that had the stage of rows
         if (!(ok = waits(&sm.loaded[st], phase, wait_ns))) break;
         const uint32_t from = from0 + st * load_bytes, to = to0 + j % kRowStages * row_bytes;
-        uint4 v[3][2];
+        if (j >= kRowStages && !(ok = waits(&sm.done[before % kRing], (before / kRing) & 1, wait_ns))) break;
+#pragma unroll 1
+        for (int i = 0; 4 * i < groups; ++i) {
 #pragma unroll
-        for (int i = 0; i < 3; ++i)
-          if (4 * i < groups) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) v[i][h] = ld_shared_v4((from + i * 32 * kLoadK) ^ (h << 6));
+          for (int h = 0; h < 2; ++h) {
+            uint32_t r[8];
+            f16_of(ld_shared_v4((from + i * 32 * kLoadK) ^ (h << 6)), r);
+            const uint32_t at = to + h * (row_bytes / 2) + i * 32 * 128;
+            st_shared_v4(at, r);
+            st_shared_v4(at ^ 16, r + 4);
           }
+        }
         __syncwarp();
         if (on) mbar_arrive(&sm.used[st]);
         if ((st += 2) >= num_stages) {
           st -= num_stages;
           phase ^= 1u;
         }
-        if (j >= kRowStages && !(ok = waits(&sm.done[before % kRing], (before / kRing) & 1, wait_ns))) break;
-#pragma unroll
-        for (int i = 0; i < 3; ++i)
-          if (4 * i < groups) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              uint32_t r[8];
-              f16_of(v[i][h], r);
-              const uint32_t at = to + h * (row_bytes / 2) + i * 32 * 128;
-              st_shared_v4(at, r);
-              st_shared_v4(at ^ 16, r + 4);
-            }
-          }
         fence_proxy_async_smem();
         arrive_with_shared_at(full0 + 8u * (j % kRing), on);
       }

@@ -10,7 +10,7 @@ namespace moe {
 
 namespace {
 
-constexpr int kQuantThreads = 256;
+constexpr int kQuantThreads = 128;  // of a block, where a row takes no more (32768 x 2048 bf16: 30.4 us, with 256 34.0, with 512 31.1)
 constexpr unsigned kAll = 0xffffffffu;
 
 // Eight elements as fp32.

@@ -44,7 +44,8 @@ constexpr int kTmemColumns = 512;
 constexpr int kStageColumns = kLoadK / 2;     // a load's features as f16
 constexpr int kThreads = 768;
 constexpr int kChunk = 32;                    // rows that leave together
-constexpr int kChunkBytes = kChunk * 256;     // 128 features in bf16
+constexpr int kPitch = 272;                   // bytes of a row's 128 features in bf16, and 16 so that eight rows lie in all banks
+constexpr int kChunkBytes = kChunk * kPitch;
 
 __device__ int32_t g_expert_i8_status;  // MOE_OK, or MOE_ERR_TIMEOUT once a wait gave up
 
@@ -172,17 +173,26 @@ __device__ __forceinline__ void f16_of(uint4 v, uint32_t* r) {
 __device__ __forceinline__ int tiles_of(int rows) { return (rows + kTileN - 1) / kTileN; }
 __device__ __forceinline__ int width_of(int rows, int tiles) { return ((rows + tiles - 1) / tiles + 31) / 32 * 32; }
 
-// A feature's gate is in the lane whose bit 3 is clear, its up eight lanes on.
-// Of the 32 rows that both hold, the lower lane gets gate and up of the even
-// ones, the upper lane those of the odd ones.
-__device__ __forceinline__ void pair_up(const float (&v)[32], bool upper, float (&g)[16], float (&u)[16]) {
+// 16 lanes x 32 columns of accumulators as a matrix product's fragment: v[4j]
+// and v[4j + 1] are lane l / 4's columns 8j + 2 (l % 4) and the next, v[4j + 2]
+// and v[4j + 3] lane l / 4 + 8's.
+__device__ __forceinline__ void tmem_load16x32(uint32_t addr, float (&v)[16]) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(addr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const float give = upper ? v[2 * i] : v[2 * i + 1], keep = upper ? v[2 * i + 1] : v[2 * i];
-    const float got = __shfl_xor_sync(0xffffffffu, give, 8);
-    g[i] = upper ? got : keep;
-    u[i] = upper ? keep : got;
-  }
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+// Four 8 x 8 matrices of 16-bit values, each lane with two of a column, to the
+// rows whose addresses lanes 8m .. 8m + 7 give for matrix m.
+__device__ __forceinline__ void store_transposed(uint32_t row, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(row), "r"(a), "r"(b), "r"(c), "r"(d)
+               : "memory");
 }
 
 // What all lanes of a warp hold alike, in a form that tells the compiler so:
@@ -463,9 +473,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_expert_i8(ExpertI8Params p, con
     const int quarter = warp & 3, tid = (int)threadIdx.x - 20 * 32;
     const uint32_t on = elect_one();
     const uint32_t acc_empty0 = in_block(&sm.acc_empty[0], 0);
-    const bool upper = lane & 8;  // holds up
-    // this lane's feature of the block's
-    const int here = GLU ? quarter * 16 + (lane >> 4) * 8 + (lane & 7) : quarter * 32 + lane;
+    // Of 16 tensor-memory lanes, two halves of a warp's, this lane has features
+    // g and g + 8 (of gate and up feature g each), and of each eight rows two.
+    const int g = lane >> 2, pair_of = (lane & 3) * 2;
+    constexpr int kPieces = GLU ? 8 : 16, kAtOnce = 128 / kPieces;  // of eight features in a row; rows stored at once
+    const int piece = tid % kPieces * 8, first_row = tid / kPieces;
+    const uint32_t buf = smem_u32(leaving);
+    // where this lane's row of what it stores transposed begins
+    const uint32_t row_of = GLU ? buf + lane * kPitch + quarter * 32
+                                : buf + ((lane >> 4) * 8 + (lane & 7)) * kPitch + (quarter * 32 + (lane & 8)) * 2;
     int acc = 0;
     for (int t = pair, jump = turn; t < num_tiles; t += jump, jump = 2 * pairs - jump) {
       find(t, o);
@@ -476,53 +492,61 @@ __global__ void __launch_bounds__(kThreads, 1) k_expert_i8(ExpertI8Params p, con
       const int nf = min(max(N - f, 0), own);          // that exist, a multiple of 8
       const int valid = min(o.n, o.rows - o.n0);       // rows of the tile that the expert has
       const int64_t row0 = (int64_t)o.lo + o.n0;
-      // scales, while the products run: the lane's feature's, and the rows'
+      // scales, while the products run: the lane's features', and the rows'
       // (read behind the vote below)
-      float sw = 0.0f;
-      if (here < nf) sw = p.w_scales[(int64_t)o.e * (GLU ? 2 * N : N) + (GLU && upper ? N : 0) + f + here];
+      float sw[2][2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int at = GLU ? quarter * 16 + h * 8 + g : quarter * 32 + h * 16 + i * 8 + g;  // feature of the block
+          sw[h][i] = at < nf ? p.w_scales[(int64_t)o.e * (GLU ? 2 * N : N) + (GLU ? i * N : 0) + f + at] : 0.0f;
+        }
       for (int i = tid; i < o.n; i += 128) sm.row_scales[as][i] = i < valid ? p.x_scales[(row0 + i) * p.x_scale_stride] : 0.0f;
       ok = epilogue_agrees(waits(&sm.acc_full[as], (uint32_t)((acc / 2) & 1), wait_ns));
       if (!ok) break;
       tmem_fence_after();
       const uint32_t src = tmem + (uint32_t)(quarter * 32) * 65536u + as * acc_columns;
+      uint8_t* to = p.out + ((row0 + first_row) * N + f + piece) * 2;
+#pragma unroll 1
       for (int c = 0; c < o.n; c += kChunk) {
         // features to rows through shared memory
-        float v[32];
-        tmem_load32(src + c, v);
-        if (c + kChunk >= o.n) {  // the last columns have been read: the accumulator is free
-          tmem_fence_before();
-          __syncwarp();
-          arrive_local_at(acc_empty0 + 8u * as, on);
-        }
-        const float4* sx = reinterpret_cast<const float4*>(sm.row_scales[as] + c);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float4 s = sx[i];
-          v[4 * i] *= s.x * sw;
-          v[4 * i + 1] *= s.y * sw;
-          v[4 * i + 2] *= s.z * sw;
-          v[4 * i + 3] *= s.w * sw;
-        }
         if (c != 0) epilogue_sync();  // the rows before have been read (the tile's before: at the vote)
-        if (GLU) {
-          float g[16], u[16];
-          pair_up(v, upper, g, u);
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
-            reinterpret_cast<uint16_t*>(leaving + (2 * i + (upper ? 1 : 0)) * 256)[here] =
-                (uint16_t)pack_bf16x2_rn(swiglu_of(g[i], u[i]), 0.0f);
-        } else {
+        for (int h = 0; h < 2; ++h) {
+          float v[16];
+          tmem_load16x32(src + (uint32_t)(h * 16) * 65536u + c, v);
+          if (h == 1 && c + kChunk >= o.n) {  // the last columns have been read: the accumulator is free
+            tmem_fence_before();
+            __syncwarp();
+            arrive_local_at(acc_empty0 + 8u * as, on);
+          }
+          uint32_t low[4], high[4];
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            reinterpret_cast<uint16_t*>(leaving + i * 256)[here] = (uint16_t)pack_bf16x2_rn(v[i], 0.0f);
+          for (int j = 0; j < 4; ++j) {
+            const float2 sx = *reinterpret_cast<const float2*>(&sm.row_scales[as][c + 8 * j + pair_of]);
+            const float a0 = v[4 * j] * (sx.x * sw[h][0]), a1 = v[4 * j + 1] * (sx.y * sw[h][0]);
+            const float b0 = v[4 * j + 2] * (sx.x * sw[h][1]), b1 = v[4 * j + 3] * (sx.y * sw[h][1]);
+            if (GLU) {
+              low[j] = pack_bf16x2_rn(swiglu_of(a0, b0), swiglu_of(a1, b1));
+            } else {
+              low[j] = pack_bf16x2_rn(a0, a1);
+              high[j] = pack_bf16x2_rn(b0, b1);
+            }
+          }
+          if (GLU) {
+            store_transposed(row_of + h * 16, low[0], low[1], low[2], low[3]);
+          } else {
+            store_transposed(row_of + h * 32, low[0], high[0], low[1], high[1]);
+            store_transposed(row_of + h * 32 + 16 * kPitch, low[2], high[2], low[3], high[3]);
+          }
         }
         epilogue_sync();
-        constexpr int kPieces = GLU ? 8 : 16;  // of eight features, in a row
 #pragma unroll
-        for (int j = 0; j < kChunk * kPieces / 128; ++j) {
-          const int i = j * 128 + tid, r = i / kPieces, at = i % kPieces * 8;
-          if (c + r < valid && at < nf)
-            st_v4(p.out + ((row0 + c + r) * N + f + at) * 2, *reinterpret_cast<const uint4*>(leaving + r * 256 + at * 2));
+        for (int j = 0; j < kChunk / kAtOnce; ++j) {
+          const int r = c + j * kAtOnce + first_row;
+          if (r < valid && piece < nf)
+            st_v4(to + (int64_t)(c + j * kAtOnce) * N * 2, ld_shared_v4(buf + (j * kAtOnce + first_row) * kPitch + piece * 2));
         }
       }
       ++acc;

@@ -13,16 +13,31 @@
 // tiles as the bf16 products do: 256 features (M), 128 to a block, by up to 192
 // rows of one expert (N), in steps of 32. Warps 0 and 2 load features and rows
 // with TMA, 128 reduction steps at a time. Warps 4-11 turn features into f16 and
-// put them into tensor memory, from where the products take their M operand:
-// shared memory, which is what a step is short of (it would read and write 96 KB
-// of it, 64 KB this way), then holds them in 8 bits only. Warps 12-19 turn rows
-// into f16 in shared memory. Both are two sets of four warps, which take one load
-// each in turn: a load's way through a set is longer than its products. Warp 1 of
-// the even block issues tcgen05.mma for both blocks; warps 20-23 scale what is
+// put them into tensor memory, from where the products take their M operand, so
+// that shared memory holds them in 8 bits only. Warps 12-19 turn rows into f16 in
+// shared memory. Both are two sets of four warps, which take one load each in
+// turn: a load's way through a set is longer than its products. Warp 1 of the
+// even block issues tcgen05.mma for both blocks; warps 20-23 scale what is
 // finished and store it.
-// Tensor memory holds two accumulators of 192 columns, so that a tile's
-// epilogue runs beside the next one's products, and four stages of features of
-// 32 columns.
+//
+// Tensor memory holds two accumulators as wide as the call's widest tile, so that
+// a tile's epilogue runs beside the next one's products, and in the rest of its
+// 512 columns features: two loads of them beside tiles of 192 rows (tiles of 160
+// and 128 leave room for three and four, and are slower: 680 and 727 us for 655
+// with the 16384 rows below), seven beside 32. Shared memory is shared out in the
+// same way, so that few rows leave room for ten loads of weights under way.
+//
+// What bounds it. Many rows: shared memory. A load of a tile of n rows moves 32 KB
+// of features (in by TMA, out to the converters) and 384 n bytes of rows (64 n in,
+// 64 n out, 128 n in as f16, 128 n out to the tensor cores) through a block's, at
+// 128 bytes a cycle 256 + 3 n cycles; its products take 4 n. So full tiles are near
+// both bounds (779 cycles a load measured, 768 the products) and narrower ones
+// at the first (160 rows 776, 128 rows 660). Without tensor memory for the
+// features it would be 768 + 3 n. Long runs meet the power cap besides (1.4 kW at 1.7 GHz).
+// 7168 -> 2 x 2048: 4608 rows in 8 experts of 576 run at 1630 TFLOP/s (166 us),
+// 16384 rows in 32 experts of 410 to 614 at 1450 to 1560 (618 to 665 us by GPU;
+// in bf16 691 to 726); 12345 uneven rows 2048 -> 7168 at 1370 to 1430 (254 to 265).
+// Few rows: the weights, 256 rows in 32 experts 144 to 149 us (941 MB, 6.4 TB/s).
 #include <mutex>
 
 #include "tcgen05.cuh"
@@ -65,7 +80,7 @@ struct Control {
   uint64_t full[kRing], done[kRing];
   uint32_t tmem;
   int32_t width;  // of the widest tile
-  alignas(16) float row_scales[2][kTileN];  // read four at a time
+  alignas(8) float row_scales[2][kTileN];  // read two at a time
 };
 constexpr size_t smem_bytes(int experts) {
   return 1024 + (size_t)kStageBytes + kChunkBytes + sizeof(Control) + ((size_t)experts + 1) * 4;
@@ -643,7 +658,7 @@ cudaError_t launch(const ExpertI8Params& p, cudaStream_t s) {
 // A few rows go to a kernel that streams the weights, if there are no more than
 // two for each expert on average: it takes two at a time and reads the weights
 // again for more, and tiles take the same time for 1 to 32. (First product 7168
-// -> 2 x 2048, here / there: 1 row 25 / 9 us, 8 rows in 8 experts 48 / 37, 16 in
+// -> 2 x 2048, here / there: 1 row 25 / 7 us, 8 rows in 8 experts 48 / 37, 16 in
 // 16 86 / 72, in 8 48 / 37, in one 24 / 87; 32 in 32 145 / 134, in 8 48 / 70.)
 bool few(const ExpertI8Params& p) { return p.rows <= kFewRows && p.rows <= 2 * (int64_t)p.num_experts; }
 

@@ -9,6 +9,14 @@
 // lanes at the end. The next piece of w is under way before the last one is
 // multiplied, across units. Where there are fewer units than warps, 2 or 4 warps
 // share one and add up in shared memory.
+//
+// What bounds it: memory. One token's first product (8 experts, 7168 -> 2 x 2048,
+// 235 MB) takes 37.5 us (6.3 TB/s), its second (2048 -> 7168, 117 MB) 19.4. Four
+// blocks an SM, a piece of four rows each way: three or two blocks 42 and 46 us,
+// with a second piece under way 44 to 52 (registers). Whole 512 bytes of a row
+// count: 64 bytes of eight rows at a time, as a matrix product's fragment wants
+// them, came to 47 us, and the integer matrix instruction on them to 45 (it is
+// slow on this chip, 60% busy with one row of eight in use).
 #include "moe_internal.cuh"
 
 namespace moe {

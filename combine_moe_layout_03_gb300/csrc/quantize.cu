@@ -4,6 +4,9 @@
 //
 // Every value is read once: a row stays in the registers of the threads that
 // share it while its largest magnitude is found, and its codes leave from there.
+// What bounds it: memory (32768 x 2048 bf16 30.4 us, 201 MB at 6.6 TB/s; 32768 x
+// 7168 fp32 164 us, 1.17 GB at 7.2 TB/s, more reads than a copy has), and the
+// launch for a few rows (2.4 us).
 #include "moe_internal.cuh"
 
 namespace moe {
@@ -121,6 +124,8 @@ cudaError_t launch(const QuantParams& p, cudaStream_t s) {
 
 }  // namespace
 
+// As few threads to a row as hold it in four or eight pieces of eight elements
+// each (2048 wide, in blocks of 256: a warp to a row 34.0 us, two 33.6, four 36.7).
 cudaError_t launch_quantize(const QuantParams& p, cudaStream_t s) {
   const int vecs = p.width / 8;
   if (vecs <= 32 * 4) return launch<32, 4>(p, s);

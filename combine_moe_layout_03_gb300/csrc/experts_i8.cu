@@ -27,17 +27,19 @@
 // with the 16384 rows below), seven beside 32. Shared memory is shared out in the
 // same way, so that few rows leave room for ten loads of weights under way.
 //
-// What bounds it. Many rows: shared memory. A load of a tile of n rows moves 32 KB
-// of features (in by TMA, out to the converters) and 384 n bytes of rows (64 n in,
-// 64 n out, 128 n in as f16, 128 n out to the tensor cores) through a block's, at
-// 128 bytes a cycle 256 + 3 n cycles; its products take 4 n. So full tiles are near
-// both bounds (779 cycles a load measured, 768 the products) and narrower ones
-// at the first (160 rows 776, 128 rows 660). Without tensor memory for the
-// features it would be 768 + 3 n. Long runs meet the power cap besides (1.4 kW at 1.7 GHz).
-// 7168 -> 2 x 2048: 4608 rows in 8 experts of 576 run at 1630 TFLOP/s (166 us),
-// 16384 rows in 32 experts of 410 to 614 at 1450 to 1560 (618 to 665 us by GPU;
-// in bf16 691 to 726); 12345 uneven rows 2048 -> 7168 at 1370 to 1430 (254 to 265).
-// Few rows: the weights, 256 rows in 32 experts 144 to 149 us (941 MB, 6.4 TB/s).
+// What bounds it. Many rows: three things that are close together. A load of a
+// tile of n rows takes 4 n cycles in the tensor cores. It moves 32 KB of features
+// (in by TMA, out to the converters) and 384 n bytes of rows (64 n in, 64 n out,
+// 128 n in as f16, 128 n out to the tensor cores) through a block's shared memory,
+// at 128 bytes a cycle 256 + 3 n cycles (768 + 3 n, were the features as f16
+// there too). And it is 600 instructions for each of an SM's schedulers at 192
+// rows, 300 of them the conversions. Full tiles take 990 cycles a load, 768 of
+// them the products'. Long runs meet the power cap besides: 16384 rows in 32
+// experts of 410 to 614, 7168 -> 2 x 2048, hold 1.4 kW and 1657 of 2070 MHz, 618 to
+// 665 us by GPU (1450 to 1560 TFLOP/s; in bf16 691 to 726 us). 4608 rows in 8
+// experts run at 1690 TFLOP/s in short runs and 1600 in long ones, 12345 uneven
+// rows 2048 -> 7168 at 1370 to 1440 (251 to 265 us).
+// Few rows: the weights, 256 rows in 32 experts 143 to 149 us (941 MB, 6.3 to 6.6 TB/s).
 #include <mutex>
 
 #include "tcgen05.cuh"
@@ -413,31 +415,28 @@ __global__ void __launch_bounds__(kThreads, 1) k_expert_i8(ExpertI8Params p, con
     const int quarter = warp & 3, set = (warp - 12) >> 2;
     const uint32_t on = elect_one();
     const uint32_t full0 = in_block(&sm.full[0], 0);
-    // eight rows x four pieces of a step at a time, each piece to two of f16
-    const uint32_t r8 = lane & 7, piece = lane >> 3, row = quarter * 8 + r8;
-    const uint32_t from0 = loads_mem + kBytesA + row * kLoadK + ((piece ^ r8) << 4);
-    const uint32_t to0 = rows_mem + row * 128 + (((2 * piece) ^ r8) << 4);
+    // eight rows x four pieces of a step at a time, each piece to two of f16:
+    // this warp has each second eight rows, of one of the two steps
+    const uint32_t r8 = lane & 7, piece = lane >> 3, row = (quarter >> 1) * 8 + r8, h = quarter & 1;
+    const uint32_t from0 = loads_mem + kBytesA + row * kLoadK + (((4 * h + piece) ^ r8) << 4);
+    const uint32_t to0 = rows_mem + h * (row_bytes / 2) + row * 128 + (((2 * piece) ^ r8) << 4);
     uint32_t j = set, tiles_end = 0;
     uint32_t st = set, phase = 0;
     for (int t = pair, jump = turn; ok && t < num_tiles; t += jump, jump = 2 * pairs - jump) {
       find(t, o);
       if (o.n <= 0) continue;
-      const int groups = o.n / 16 - quarter;  // of eight rows, each fourth of them this warp's
       for (tiles_end += num_loads; j < tiles_end; j += 2) {
         const uint32_t before = j - kRowStages;  // the load that had the stage of rows
         if (!(ok = waits(&sm.loaded[st], phase, wait_ns))) break;
         const uint32_t from = from0 + st * load_bytes, to = to0 + j % kRowStages * row_bytes;
         if (j >= kRowStages && !(ok = waits(&sm.done[before % kRing], (before / kRing) & 1, wait_ns))) break;
 #pragma unroll 1
-        for (int i = 0; 4 * i < groups; ++i) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t r[8];
-            f16_of(ld_shared_v4((from + i * 32 * kLoadK) ^ (h << 6)), r);
-            const uint32_t at = to + h * (row_bytes / 2) + i * 32 * 128;
-            st_shared_v4(at, r);
-            st_shared_v4(at ^ 16, r + 4);
-          }
+        for (int i = 0; i < o.n / 32; ++i) {
+          uint32_t r[8];
+          f16_of(ld_shared_v4(from + i * 16 * kLoadK), r);
+          const uint32_t at = to + i * 16 * 128;
+          st_shared_v4(at, r);
+          st_shared_v4(at ^ 16, r + 4);
         }
         __syncwarp();
         if (on) mbar_arrive(&sm.used[st]);

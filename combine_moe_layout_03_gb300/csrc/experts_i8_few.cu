@@ -45,7 +45,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) k_expert_i8_few(ExpertI8Par
   __shared__ int32_t busy[kFewRows][3];  // experts with rows: index, first row, rows
   __shared__ int32_t num_busy;
   __shared__ int32_t part[kWarps][kRows][kUnit];
-  const int warp = threadIdx.x >> 5, lane = (int)lane_id();
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = (int)lane_id();
   const int E = p.num_experts, K = p.in_features, N = p.out_features;
   pdl_wait();
   pdl_trigger();
@@ -122,12 +122,12 @@ __global__ void __launch_bounds__(kThreads, kBlocks) k_expert_i8_few(ExpertI8Par
           for (int i = 0; i < kUnit; ++i) acc[r][i] = dot16(v.w[i], c, acc[r][i]);
         }
       }
-#pragma unroll
-      for (int r = 0; r < kRows; ++r)
-        if (r < rows)
-#pragma unroll
-          for (int i = 0; i < kUnit; ++i) acc[r][i] = __reduce_add_sync(0xffffffffu, acc[r][i]);
       if (S > 1) {
+#pragma unroll
+        for (int r = 0; r < kRows; ++r)
+          if (r < rows)
+#pragma unroll
+            for (int i = 0; i < kUnit; ++i) acc[r][i] = __reduce_add_sync(0xffffffffu, acc[r][i]);
         const int barrier = 1 + warp / S;  // of the unit's warps
         if (own > 0 && lane == 0) {
 #pragma unroll
@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) k_expert_i8_few(ExpertI8Par
         float y[kUnit];
         const float sx = p.x_scales[(row0 + r) * p.x_scale_stride];
 #pragma unroll
-        for (int i = 0; i < kUnit; ++i) y[i] = __int2float_rn(acc[r][i]) * (sx * sw[GLU ? i / 2 * N + i % 2 : i]);
+        for (int i = 0; i < kUnit; ++i) y[i] = __int2float_rn(S > 1 ? acc[r][i] : __reduce_add_sync(0xffffffffu, acc[r][i])) * (sx * sw[GLU ? i / 2 * N + i % 2 : i]);
         uint8_t* to = p.out + ((row0 + r) * N + f) * 2;
         if (lane == 0) {
           if (GLU)

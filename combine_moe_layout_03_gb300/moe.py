@@ -1194,6 +1194,8 @@ def moe_quantize_rows(desc: MoeQuantDesc, x, q=None, scales=None, num_rows=None,
 def _prepare_expert_i8(name: str, desc: MoeExpertI8Desc, halves: int, x, x_scales, row_begin, row_end, w, w_scales, out,
                        stream) -> Prepared:
     e, r, k, n = desc.num_experts, desc.rows, desc.in_features, desc.out_features
+    if x_scales is not None and x_scales.dim() == 2 and x_scales.shape[1]:  # as moe_quantize_rows returns them: the first of each row
+        x_scales = x_scales[:, 0]
     _want("row_begin", row_begin, torch.int32, e)
     _want("row_end", row_end, torch.int32, e)
     _want_rows("x", x, torch.int8, r, k, desc.x_stride or k)

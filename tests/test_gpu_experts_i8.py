@@ -183,7 +183,7 @@ def test_quantise_products_and_back(moe, scale_width):
     q1, s1 = moe.moe_quantize_rows(moe.MoeQuantDesc(e * 2 * f, h), w1)
     q2, s2 = moe.moe_quantize_rows(moe.MoeQuantDesc(e * h, f), w2)
     q, s = moe.moe_quantize_rows(moe.MoeQuantDesc(rows, h, scale_stride=scale_width), x)
-    act = moe.moe_expert_swiglu_i8(moe.MoeExpertI8Desc(e, rows, h, f, x_scale_stride=scale_width), q, s[:, 0], begin, end, q1, s1)
+    act = moe.moe_expert_swiglu_i8(moe.MoeExpertI8Desc(e, rows, h, f, x_scale_stride=scale_width), q, s, begin, end, q1, s1)
     qa, sa = moe.moe_quantize_rows(moe.MoeQuantDesc(rows, f), act)
     y = moe.moe_expert_product_i8(moe.MoeExpertI8Desc(e, rows, f, h), qa, sa, begin, end, q2, s2)
     def scaled(q, s, w, sw):  # sums of whole numbers, which are exact in 64 bits (a sum of scaled ones is not: where it is zero, say)

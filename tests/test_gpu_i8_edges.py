@@ -118,6 +118,29 @@ def test_few_rows_from_records(moe):
     assert torch.equal(y[inside], ref[inside]) and bool((y[outside] == 9.0).all())
 
 
+def test_few_rows_with_scales_that_are_not_numbers(moe):
+    rows, cin, n = 5, 64, 136
+    begin, end = ranges([2, 0, 3], DEV)
+    x, w, sx, sw = codes(1, rows, cin), codes(2, 3, n, cin), scales(3, rows), scales(4, 3, n)
+    sx[1], sw[2, 9] = float("nan"), float("inf")
+    y = moe.moe_expert_product_i8(moe.MoeExpertI8Desc(3, rows, cin, n), x, sx, begin, end, w, sw)
+    ref = product_of(x, sx, begin, end, w, sw)
+    assert torch.equal(y.isnan(), ref.isnan()) and torch.equal(y.nan_to_num(), ref.nan_to_num())
+    assert bool(y[1].isnan().all()) and not bool(y[[0, 2, 3, 4]].isnan().any(1).all())
+
+
+def test_a_row_that_is_not_finite_is_nan_to_the_end(moe):
+    # quantised to the scale NaN, carried through the product
+    for rows in (3, 40):
+        x = torch.randn(rows, 128, device=DEV).bfloat16()
+        x[1, 17] = float("inf")
+        w, sw = codes(2, 2, 64, 128), scales(4, 2, 64)
+        begin, end = ranges([2, rows - 2], DEV)
+        q, s = moe.moe_quantize_rows(moe.MoeQuantDesc(rows, 128), x)
+        y = moe.moe_expert_product_i8(moe.MoeExpertI8Desc(2, rows, 128, 64), q, s, begin, end, w, sw)
+        assert bool(y[1].isnan().all()) and not bool(y[0].isnan().any()) and not bool(y[2:].isnan().any())
+
+
 @pytest.mark.parametrize("most", [1, 3, 70])
 def test_the_most_experts(moe, most):
     g = torch.Generator()

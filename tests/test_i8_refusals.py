@@ -115,6 +115,11 @@ def test_python_checks_of_products(moe, halves):
             ("w_scales", gpu(e, halves * n - 1, dtype=torch.float32), CAPACITY), ("w_scales", None, INVALID), ("x", None, INVALID),
             (last, gpu(r, n, dtype=torch.float32), INVALID), (last, gpu(r - 1, n, dtype=torch.bfloat16), CAPACITY)):
         assert code_of(moe, call, d, **{**good, last: out, name: bad}) == code, name
+    # scales [rows, scale_stride] count as the first of each row, at the stride that the desc gives
+    four = moe.MoeExpertI8Desc(e, r, k, n, x_scale_stride=4)
+    assert code_of(moe, call, d, **{**good, last: out, "x_scales": gpu(r, 4, dtype=torch.float32)}) == INVALID
+    assert code_of(moe, call, four, **{**good, last: out, "x_scales": gpu(r, 1, dtype=torch.float32)}) == INVALID
+    assert code_of(moe, call, four, **{**good, last: out, "x_scales": gpu(r - 1, 4, dtype=torch.float32)}) == CAPACITY
     strided = moe.MoeExpertI8Desc(e, r, k, n, x_stride=48, x_scale_stride=12)
     assert code_of(moe, call, strided, **{**good, last: out}) == INVALID
 

@@ -297,11 +297,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_expert_i8(ExpertI8Params p, con
   const int num_tiles = uniform(first[E]) * across;
   const int num_loads = (K + kLoadK - 1) / kLoadK;                                // of every tile
   const bool short_end = K - (num_loads - 1) * kLoadK <= kStepK;                  // the last load is one step
-  // The t-th tile; o is this warp's tile before, or has e = -1.
+  // The t-th tile; o is this warp's tile before, or has e = -1. (A lane looks at
+  // one of the next 32 experts: one by one, 248 without rows before eight with 8
+  // rows each took 8 of 36 us.)
   auto find = [&](int t, Tile& o) {
     const int before = o.e;
     o.e = max(o.e, 0);
-    while (t >= uniform(first[o.e + 1]) * across) ++o.e;
+    for (;; o.e += 32) {
+      const unsigned has = __ballot_sync(0xffffffffu, o.e + lane < E && t < first[min(o.e + lane, E - 1) + 1] * across);
+      if (has) {
+        o.e += __ffs((int)has) - 1;
+        break;
+      }
+    }
     if (o.e != before) {
       int lo;
       o.rows = uniform(rows_of(o.e, lo));

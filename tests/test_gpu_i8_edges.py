@@ -153,6 +153,18 @@ def test_the_most_experts(moe, most):
     assert torch.equal(y, product_of(x, sx, begin, end, w, sw))
 
 
+@pytest.mark.parametrize("busy", [[0], [31, 32], [33, 500, 1023], [1023], [255, 256, 257, 800]], ids=str)
+def test_many_experts_without_rows(moe, busy):
+    counts = [0] * 1024
+    for i, e in enumerate(busy):
+        counts[e] = 20 + 200 * (i % 2)
+    rows, cin, n = sum(counts), 144, 520
+    begin, end = ranges(counts, DEV)
+    x, w, sx, sw = codes(1, rows, cin), codes(2, 1024, n, cin), scales(3, rows), scales(4, 1024, n)
+    y = moe.moe_expert_product_i8(moe.MoeExpertI8Desc(1024, rows, cin, n), x, sx, begin, end, w, sw)
+    assert torch.equal(y, product_of(x, sx, begin, end, w, sw))
+
+
 @pytest.mark.parametrize("width", [32, 64, 96, 128, 160, 192])
 def test_every_width_of_tiles(moe, width):
     # the widest tile sets how many stages there are; many steps go around all of them

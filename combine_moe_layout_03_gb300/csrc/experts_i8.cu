@@ -39,7 +39,7 @@
 // 665 us by GPU (1450 to 1560 TFLOP/s; in bf16 691 to 726 us). 4608 rows in 8
 // experts run at 1690 TFLOP/s in short runs and 1600 in long ones, 12345 uneven
 // rows 2048 -> 7168 at 1370 to 1440 (251 to 265 us).
-// Few rows: the weights, 256 rows in 32 experts 143 to 149 us (941 MB, 6.3 to 6.6 TB/s).
+// Few rows: the weights, 256 rows in 32 experts 142 to 149 us (941 MB, 6.3 to 6.6 TB/s).
 #include <mutex>
 
 #include "tcgen05.cuh"
@@ -248,8 +248,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_expert_i8(ExpertI8Params p, con
   if (threadIdx.x >= 32 && threadIdx.x < 36)  // for the first copies
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<const CUtensorMap*>(&maps) + (threadIdx.x - 32)) : "memory");
   __syncthreads();
-  // (both blocks run before either allocates: the allocation works in both)
-  cluster_sync();
+  // (both blocks run before either allocates: the allocation works in both; the
+  // fence behind the barriers' initialisation is what orders them for the other)
+  cluster_meet();
   if (warp == 1) tmem_alloc(&sm.tmem, kTmemColumns);
   pdl_wait();
   pdl_trigger();
@@ -582,7 +583,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_expert_i8(ExpertI8Params p, con
   tmem_fence_after();
   if (warp == 1) tmem_free(tmem, kTmemColumns);
   __syncwarp();
-  cluster_sync();  // and neither leaves before both have freed theirs
+  cluster_meet();  // and neither leaves before both have freed theirs
 }
 
 // int8 in boxes of 128 bytes x `rows`; what lies outside reads as zero.

@@ -16,6 +16,11 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+// The same without an order of memory: neither block goes on before all of both
+// have come. (cluster_sync takes some 1000 cycles more.)
+__device__ __forceinline__ void cluster_meet() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
 // One lane of a warp that runs together. The operations below that one thread
 // issues are predicated on it instead of standing behind a branch: the warp
 // then stays together and their operands in uniform registers. (Behind `if

@@ -16,9 +16,10 @@
 // put them into tensor memory, from where the products take their M operand, so
 // that shared memory holds them in 8 bits only. Warps 12-19 turn rows into f16 in
 // shared memory. Both are two sets of four warps, which take one load each in
-// turn: a load's way through a set is longer than its products. Warp 1 of the
-// even block issues tcgen05.mma for both blocks; warps 20-23 scale what is
-// finished and store it.
+// turn: a load's way through a set is longer than its products (16384 rows below:
+// one set 1361 us for 939, when that was tried; three sets 668 for 646 now). Warp
+// 1 of the even block issues tcgen05.mma for both blocks; warps 20-23 scale what
+// is finished and store it.
 //
 // Tensor memory holds two accumulators as wide as the call's widest tile, so that
 // a tile's epilogue runs beside the next one's products, and in the rest of its
@@ -35,8 +36,8 @@
 // there too). And it is 600 instructions for each of an SM's schedulers at 192
 // rows, 300 of them the conversions. Full tiles take 990 cycles a load, 768 of
 // them the products'. Long runs meet the power cap besides: 16384 rows in 32
-// experts of 410 to 614, 7168 -> 2 x 2048, hold 1.4 kW and 1657 of 2070 MHz, 618 to
-// 665 us by GPU (1450 to 1560 TFLOP/s; in bf16 691 to 726 us). 4608 rows in 8
+// experts of 410 to 614, 7168 -> 2 x 2048, hold 1.4 kW and 1657 of 2070 MHz, 600 to
+// 665 us by GPU (1450 to 1600 TFLOP/s; in bf16 691 to 726 us). 4608 rows in 8
 // experts run at 1690 TFLOP/s in short runs and 1600 in long ones, 12345 uneven
 // rows 2048 -> 7168 at 1370 to 1440 (251 to 265 us).
 // Few rows: the weights, 256 rows in 32 experts 142 to 149 us (941 MB, 6.3 to 6.6 TB/s).

@@ -665,11 +665,13 @@ cudaError_t launch(const ExpertI8Params& p, cudaStream_t s) {
 }
 
 // A few rows go to a kernel that streams the weights, if there are no more than
-// two for each expert on average: it takes two at a time and reads the weights
-// again for more, and tiles take the same time for 1 to 32. (First product 7168
-// -> 2 x 2048, here / there: 1 row 25 / 7 us, 8 rows in 8 experts 48 / 37, 16 in
-// 16 86 / 72, in 8 48 / 37, in one 24 / 87; 32 in 32 145 / 134, in 8 48 / 70.)
-bool few(const ExpertI8Params& p) { return p.rows <= kFewRows && p.rows <= 2 * (int64_t)p.num_experts; }
+// some two for each expert on average: it takes two at a time and reads the
+// weights again (from L2) for more, and tiles take the same time for 1 to 32. The
+// counts of each expert are not known here. (First product 7168 -> 2 x 2048, tiles /
+// streamed: 1 row 25 / 7 us, 4 rows of one expert 24 / 12, 8 24 / 19, 16 24 / 35; 8
+// rows in 8 experts 48 / 37, 16 in 16 86 / 74, in 8 48 / 38; 32 in 32 145 / 134, in
+// 8 48 / 70. Second product: 8 rows of one expert 10 / 11 us.)
+bool few(const ExpertI8Params& p) { return p.rows <= kFewRows && p.rows <= 2 * (int64_t)p.num_experts + 4; }
 
 }  // namespace
 

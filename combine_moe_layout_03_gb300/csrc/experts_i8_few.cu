@@ -40,40 +40,23 @@ __device__ __forceinline__ int32_t dot16(uint4 a, uint4 b, int32_t c) {
   return __dp4a((int)a.w, (int)b.w, c);
 }
 
+constexpr int features_of(bool glu) { return glu ? kUnit / 2 : kUnit; }  // of a unit
+
+struct Shared {
+  int32_t busy[kFewRows][3];  // experts with rows: index, first row, rows
+  int32_t num_busy;
+  int32_t part[kWarps][kRows][kUnit];
+};
+
 // S: warps to a unit.
 template <bool GLU, int S>
-__global__ void __launch_bounds__(kThreads, kBlocks) k_expert_i8_few(ExpertI8Params p) {
-  __shared__ int32_t busy[kFewRows][3];  // experts with rows: index, first row, rows
-  __shared__ int32_t num_busy;
-  __shared__ int32_t part[kWarps][kRows][kUnit];
-  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = (int)lane_id();
-  const int E = p.num_experts, K = p.in_features, N = p.out_features;
-  pdl_wait();
-  pdl_trigger();
-  if (warp == 0) {
-    int many = 0;
-    for (int e0 = 0; e0 < E; e0 += 32) {
-      const int e = e0 + lane;
-      int lo = 0, rows = 0;
-      if (e < E) {
-        lo = max(p.row_begin[e], 0);
-        rows = (int)min((int64_t)max(p.row_end[e], 0), p.rows) - lo;
-      }
-      const unsigned some = __ballot_sync(0xffffffffu, rows > 0);
-      const int at = many + __popc(some & ((1u << lane) - 1));
-      if (rows > 0 && at < kFewRows) {
-        busy[at][0] = e;
-        busy[at][1] = lo;
-        busy[at][2] = rows;
-      }
-      many += __popc(some);
-    }
-    if (lane == 0) num_busy = min(many, kFewRows);
-  }
-  __syncthreads();
-  constexpr int kFeatures = GLU ? kUnit / 2 : kUnit;  // of a unit
+__device__ __forceinline__ void work_on(const ExpertI8Params& p, Shared& sm, int warp, int lane) {
+  const int32_t(&busy)[kFewRows][3] = sm.busy;
+  int32_t(&part)[kWarps][kRows][kUnit] = sm.part;
+  const int K = p.in_features, N = p.out_features;
+  constexpr int kFeatures = features_of(GLU);
   const int groups = N / kFeatures;                   // units of an expert
-  const int units = num_busy * groups, step = gridDim.x * (kWarps / S);
+  const int units = sm.num_busy * groups, step = gridDim.x * (kWarps / S);
   const int first = warp / S * gridDim.x + blockIdx.x;  // this warp's first unit: the last ones are spread over the SMs
   const int own = warp % S;                             // its pieces: own, own + S, ...
   const int end = (K + kPiece - 1) / kPiece * kPiece, begin = own * kPiece + lane * 16;
@@ -172,18 +155,51 @@ __global__ void __launch_bounds__(kThreads, kBlocks) k_expert_i8_few(ExpertI8Par
 }
 
 template <bool GLU>
+__global__ void __launch_bounds__(kThreads, kBlocks) k_expert_i8_few(ExpertI8Params p) {
+  __shared__ Shared sm;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = (int)lane_id();
+  const int E = p.num_experts;
+  pdl_wait();
+  pdl_trigger();
+  if (warp == 0) {
+    int many = 0;
+    for (int e0 = 0; e0 < E; e0 += 32) {
+      const int e = e0 + lane;
+      int lo = 0, rows = 0;
+      if (e < E) {
+        lo = max(p.row_begin[e], 0);
+        rows = (int)min((int64_t)max(p.row_end[e], 0), p.rows) - lo;
+      }
+      const unsigned some = __ballot_sync(0xffffffffu, rows > 0);
+      const int at = many + __popc(some & ((1u << lane) - 1));
+      if (rows > 0 && at < kFewRows) {
+        sm.busy[at][0] = e;
+        sm.busy[at][1] = lo;
+        sm.busy[at][2] = rows;
+      }
+      many += __popc(some);
+    }
+    if (lane == 0) sm.num_busy = min(many, kFewRows);
+  }
+  __syncthreads();
+  // As many warps to a unit as there are for all units, which only the counts of
+  // rows tell: at most four.
+  const int units = sm.num_busy * (p.out_features / features_of(GLU)), warps = gridDim.x * kWarps;
+  if (units * 4 <= warps)
+    work_on<GLU, 4>(p, sm, warp, lane);
+  else if (units * 2 <= warps)
+    work_on<GLU, 2>(p, sm, warp, lane);
+  else
+    work_on<GLU, 1>(p, sm, warp, lane);
+}
+
+template <bool GLU>
 cudaError_t launch(const ExpertI8Params& p, int sms, cudaStream_t s) {
-  const int64_t groups = p.out_features / (GLU ? kUnit / 2 : kUnit);
-  const int64_t units = (p.rows < p.num_experts ? p.rows : p.num_experts) * groups;  // at most
-  const int64_t most = (int64_t)sms * kBlocks;
-  const int shared = units * 4 <= most * kWarps ? 4 : units * 2 <= most * kWarps ? 2 : 1;
-  const int64_t need = (units * shared + kWarps - 1) / kWarps;
-  const void* fn = shared == 4   ? (const void*)k_expert_i8_few<GLU, 4>
-                   : shared == 2 ? (const void*)k_expert_i8_few<GLU, 2>
-                                 : (const void*)k_expert_i8_few<GLU, 1>;
+  const int64_t units = (p.rows < p.num_experts ? p.rows : p.num_experts) * (p.out_features / features_of(GLU));  // at most
+  const int64_t need = (units * 4 + kWarps - 1) / kWarps, most = (int64_t)sms * kBlocks;
   ExpertI8Params q = p;
   void* args[] = {&q};
-  return launch_pdl(fn, dim3((unsigned)(need < most ? need : most)), dim3(kThreads), 0, s, args);
+  return launch_pdl((const void*)k_expert_i8_few<GLU>, dim3((unsigned)(need < most ? need : most)), dim3(kThreads), 0, s, args);
 }
 
 }  // namespace

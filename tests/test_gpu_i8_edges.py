@@ -33,9 +33,9 @@ def near_swiglu(act, v):
     return bool(((act.double() - ref).abs() <= lim).all())
 
 
-# at most 16 rows, and two for each expert on average: one expert with all of
+# at most 16 rows, and some two for each expert on average: one expert with all of
 # them, some with none, one or several units of four rows of w for each warp
-FEW = [[1], [0, 2], [0, 0, 1, 0], [1] * 16, [2, 0, 1, 5, 0, 0, 1, 1], [0, 0, 0, 0, 0, 0, 0, 16], [3, 4, 1, 0], [0] * 30 + [1, 3]]
+FEW = [[1], [6], [0, 2], [8, 0], [0, 0, 1, 0], [1] * 16, [2, 0, 1, 5, 0, 0, 1, 1], [0, 0, 0, 0, 0, 0, 0, 16], [3, 4, 1, 0], [0] * 30 + [1, 3]]
 
 
 @pytest.mark.parametrize("counts", FEW, ids=str)

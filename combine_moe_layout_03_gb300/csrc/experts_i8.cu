@@ -34,11 +34,11 @@
 // 128 n in as f16, 128 n out to the tensor cores) through a block's shared memory,
 // at 128 bytes a cycle 256 + 3 n cycles (768 + 3 n, were the features as f16
 // there too). And it is 600 instructions for each of an SM's schedulers at 192
-// rows, 300 of them the conversions. Full tiles take 990 cycles a load, 768 of
+// rows, 300 of them the conversions. Full tiles take 970 cycles a load, 768 of
 // them the products'. Long runs meet the power cap besides: 16384 rows in 32
 // experts of 410 to 614, 7168 -> 2 x 2048, hold 1.4 kW and 1657 of 2070 MHz, 600 to
 // 665 us by GPU (1450 to 1600 TFLOP/s; in bf16 691 to 726 us). 4608 rows in 8
-// experts run at 1690 TFLOP/s in short runs and 1600 in long ones, 12345 uneven
+// experts run at 1720 TFLOP/s in short runs and 1600 in long ones, 12345 uneven
 // rows 2048 -> 7168 at 1370 to 1440 (251 to 265 us).
 // Few rows: the weights, 256 rows in 32 experts 142 to 149 us (941 MB, 6.3 to 6.6 TB/s).
 #include <mutex>
@@ -52,12 +52,12 @@ namespace {
 constexpr int kTileM = 256, kTileN = 192;     // of a pair
 constexpr int kHalfM = 128;                   // of a block
 constexpr int kLoadK = 128, kStepK = 64;      // reduction steps loaded together, and multiplied together
-// Stages: of what is loaded (4 to 10, by the widest tile), of features as f16
-// (2 to 7), of rows as f16, and of barriers between converters and products,
-// which are more than stages of either.
-constexpr int kMostLoads = 10, kRowStages = 4, kRing = 8;
+// Stages: of what is loaded (5 to 10, by the widest tile; with more than some 900
+// experts 4), of features as f16 (2 to 7), of rows as f16, and of barriers between
+// converters and products, which are more than stages of either. (Four of rows
+// and of loads: full tiles 161.7 us for 158.4, tiles of 160 rows 105 for 97.)
+constexpr int kMostLoads = 10, kRowStages = 3, kRing = 8;
 constexpr int kBytesA = kHalfM * kLoadK;
-constexpr int kStageBytes = 4 * (kBytesA + kTileN / 2 * kLoadK) + kRowStages * kTileN * kLoadK;  // for all of them
 constexpr int kTmemColumns = 512;
 constexpr int kStageColumns = kLoadK / 2;     // a load's features as f16
 constexpr int kThreads = 768;
@@ -85,9 +85,12 @@ struct Control {
   int32_t width;  // of the widest tile
   alignas(8) float row_scales[2][kTileN];  // read two at a time
 };
-constexpr size_t smem_bytes(int experts) {
-  return 1024 + (size_t)kStageBytes + kChunkBytes + sizeof(Control) + ((size_t)experts + 1) * 4;
+// Shared memory: the stages have what the others leave, from a multiple of 1024 on.
+constexpr uint32_t kSharedBytes = 227 * 1024;
+constexpr uint32_t stage_bytes(int experts) {
+  return (kSharedBytes - 1024 - kChunkBytes - (uint32_t)sizeof(Control) - ((uint32_t)experts + 1) * 4) / 1024 * 1024;
 }
+static_assert(stage_bytes(MOE_MAX_EXPERTS) >= 4 * (kBytesA + kTileN / 2 * kLoadK) + kRowStages * kTileN * kLoadK, "four loads beside the widest tiles");
 
 // Named barrier of the epilogue warps, and a vote at it. It waits without a
 // limit, so whoever comes must know that the others do: a wait with a limit is
@@ -223,7 +226,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_expert_i8(ExpertI8Params p, con
   extern __shared__ uint8_t expert_raw[];
   // (an offset, so that the compiler knows these for addresses of shared memory)
   uint8_t* loads = expert_raw + (-smem_u32(expert_raw) & 1023u);
-  uint8_t* leaving = loads + kStageBytes;
+  uint8_t* leaving = loads + stage_bytes(p.num_experts);
   Control& sm = *reinterpret_cast<Control*>(leaving + kChunkBytes);
   int32_t* first = reinterpret_cast<int32_t*>(&sm + 1);  // row tiles before expert e
   const int warp = uniform(threadIdx.x >> 5), lane = (int)lane_id();
@@ -287,7 +290,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_expert_i8(ExpertI8Params p, con
   // as there is room for: the fewer rows, the more weights are under way.
   const uint32_t row_bytes = acc_columns * kLoadK;  // a load's rows as f16: two steps, one behind the other
   const uint32_t load_bytes = kBytesA + acc_columns / 2 * kLoadK;
-  const uint32_t num_stages = min((kStageBytes - kRowStages * row_bytes) / load_bytes, (uint32_t)kMostLoads);
+  const uint32_t num_stages = min((stage_bytes(E) - kRowStages * row_bytes) / load_bytes, (uint32_t)kMostLoads);
   const uint32_t loads_mem = smem_u32(loads), rows_mem = loads_mem + num_stages * load_bytes;
   const uint32_t tmem_features = tmem + 2 * acc_columns;
 
@@ -608,7 +611,7 @@ int resident_pairs(int dev, int sms) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(sms / 2 * 2));
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem_bytes(MOE_MAX_EXPERTS);
+    cfg.dynamicSmemBytes = kSharedBytes;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;
     attr.val.clusterDim.x = 2;
@@ -650,7 +653,7 @@ cudaError_t launch(const ExpertI8Params& p, cudaStream_t s) {
   }
   if (!ok) return cudaErrorUnknown;
   const void* fn = (const void*)k_expert_i8<GLU>;
-  cudaError_t err = ensure_dynamic_smem(fn, smem_bytes(MOE_MAX_EXPERTS));
+  cudaError_t err = ensure_dynamic_smem(fn, kSharedBytes);
   if (err != cudaSuccess) return err;
   const int64_t pairs = resident_pairs<GLU>(dev, sms);
   if (pairs < 1) return cudaErrorInvalidConfiguration;
@@ -660,7 +663,7 @@ cudaError_t launch(const ExpertI8Params& p, cudaStream_t s) {
   ExpertI8Params q = p;
   uint64_t wait_ns = wait_limit_ns();
   void* args[] = {&q, &maps, &wait_ns};
-  return launch_pdl(fn, dim3((unsigned)(2 * (most < pairs ? most : pairs))), dim3(kThreads), smem_bytes(p.num_experts), s,
+  return launch_pdl(fn, dim3((unsigned)(2 * (most < pairs ? most : pairs))), dim3(kThreads), kSharedBytes, s,
                     args, 2);
 }
 

@@ -157,7 +157,7 @@ def test_the_most_experts(moe, most):
 def test_many_experts_without_rows(moe, busy):
     counts = [0] * 1024
     for i, e in enumerate(busy):
-        counts[e] = 20 + 200 * (i % 2)
+        counts[e] = (20, 220, 570)[i % 3]
     rows, cin, n = sum(counts), 144, 520
     begin, end = ranges(counts, DEV)
     x, w, sx, sw = codes(1, rows, cin), codes(2, 1024, n, cin), scales(3, rows), scales(4, 1024, n)

@@ -43,6 +43,7 @@
 // Few rows: the weights, 256 rows in 32 experts 142 to 149 us (941 MB, 6.3 to 6.6 TB/s).
 #include <mutex>
 
+#include "row_tiles.h"
 #include "tcgen05.cuh"
 
 namespace moe {
@@ -189,11 +190,6 @@ __device__ __forceinline__ void f16_of(uint4 v, uint32_t* r) {
   f16_of(v.w, r + 6);
 }
 
-// Row tiles of an expert: as few as hold its rows, of equal width in steps of
-// 32; the last is as wide as what is left.
-__device__ __forceinline__ int tiles_of(int rows) { return (rows + kTileN - 1) / kTileN; }
-__device__ __forceinline__ int width_of(int rows, int tiles) { return ((rows + tiles - 1) / tiles + 31) / 32 * 32; }
-
 // 16 lanes x 32 columns of accumulators as a matrix product's fragment: v[4j]
 // and v[4j + 1] are lane l / 4's columns 8j + 2 (l % 4) and the next, v[4j + 2]
 // and v[4j + 3] lane l / 4 + 8's.
@@ -267,8 +263,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_expert_i8(ExpertI8Params p, con
     for (int e0 = 0; e0 < E; e0 += 32) {
       const int e = e0 + lane;
       int lo;
-      const int rows = e < E ? rows_of(e, lo) : 0, n = tiles_of(rows);
-      if (n > 0) width = max(width, width_of(rows, n));
+      const int rows = e < E ? rows_of(e, lo) : 0, n = row_tiles(rows, kTileN);
+      if (n > 0) width = max(width, row_tile_width(rows, n));
       const int inc = warp_inclusive_scan(n);
       if (e < E) first[e] = carry + inc - n;
       carry += __shfl_sync(0xffffffffu, inc, 31);
@@ -323,7 +319,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_expert_i8(ExpertI8Params p, con
     const int begin = uniform(first[o.e]), many = uniform(first[o.e + 1]) - begin;
     const int i = t - begin * across;
     o.f0 = i / many * tile_features;
-    const int width = width_of(o.rows, many);
+    const int width = row_tile_width(o.rows, many);
     o.n0 = i % many * width;
     o.n = min(width, (max(o.rows - o.n0, 0) + 31) / 32 * 32);
   };

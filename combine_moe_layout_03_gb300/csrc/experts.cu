@@ -43,6 +43,7 @@
 // of fp32 780 to 880 us (bf16 695 to 705, added to fp32 1483).
 #include <mutex>
 
+#include "row_tiles.h"
 #include "tcgen05.cuh"
 
 namespace moe {
@@ -153,11 +154,6 @@ constexpr size_t expert_smem(int mode, int experts) {
          (mode == kGradWeight ? 0 : ((size_t)experts + 1) * 4) + sizeof(ExpertControl) + 16;
 }
 
-
-// Row tiles of an expert: as few as hold its rows, of equal width in steps of
-// 32; the last is as wide as what is left.
-__device__ __forceinline__ int tiles_of(int rows) { return (rows + kTileN - 1) / kTileN; }
-
 // A feature's gate is in the lane whose bit 3 is clear, its up eight lanes on.
 // Of the 32 rows that both hold, the lower lane gets gate and up of the even
 // ones, the upper lane those of the odd ones.
@@ -226,7 +222,7 @@ __global__ void __launch_bounds__(kExpertThreads, 1)
     for (int e0 = 0; e0 < E; e0 += 32) {
       const int e = e0 + lane;
       int lo;
-      const int n = e < E ? tiles_of(rows_of(e, lo)) : 0;
+      const int n = e < E ? row_tiles(rows_of(e, lo), kTileN) : 0;
       const int inc = warp_inclusive_scan(n);
       if (e < E) first[e] = carry + inc - n;
       carry += __shfl_sync(0xffffffffu, inc, 31);
@@ -271,7 +267,7 @@ __global__ void __launch_bounds__(kExpertThreads, 1)
       const int many = first[o.e + 1] - first[o.e];
       const int i = t - first[o.e] * across;
       o.f0 = i / many * tile_features;
-      const int width = ((o.rows + many - 1) / many + 31) / 32 * 32;
+      const int width = row_tile_width(o.rows, many);
       o.n0 = i % many * width;
       o.n = min(width, (max(o.rows - o.n0, 0) + 31) / 32 * 32);
     }

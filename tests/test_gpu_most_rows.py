@@ -3,6 +3,7 @@ one expert (80 GB): each of them is in a tile and where it belongs."""
 import pytest
 import torch
 
+from test_gpu_experts import whole
 from test_gpu_experts_i8 import DEV, codes, scales
 from test_gpu_i8_edges import near_swiglu, product_of
 
@@ -57,4 +58,19 @@ def test_8_bit_products(moe, glu):
         assert near_swiglu(y[at], v)
     else:
         assert torch.equal(y[at], product_of(x[at], sx[at], b, t, w, sw))
+    assert rows_that_are_not_zero(y) == rows_that_are_not_zero(y[at])
+
+
+@pytest.mark.parametrize("name", ["moe_expert_product", "moe_expert_swiglu", "moe_expert_product_backward_input"])
+def test_bf16_products(moe, name):
+    at = places()
+    begin, end, b, t = ends(at)
+    x = torch.zeros(ROWS, 8, dtype=torch.bfloat16, device=DEV)
+    x[at] = whole(1, len(at), 8)
+    w = whole(3, 2, 16 if "swiglu" in name else 8, 8)
+    y = torch.full((ROWS, 8), 9.0, dtype=torch.bfloat16, device=DEV)
+    getattr(moe, name)(moe.MoeExpertDesc(2, ROWS, 8, 8), x, begin, end, w, y)
+    v = torch.cat([x[at[i:j]].double() @ (w[e] if "input" in name else w[e].t()).double()  # sums of whole numbers
+                   for e, (i, j) in enumerate(zip(b.tolist(), t.tolist()))])
+    assert near_swiglu(y[at], v) if "swiglu" in name else torch.equal(y[at], v.to(torch.bfloat16))
     assert rows_that_are_not_zero(y) == rows_that_are_not_zero(y[at])

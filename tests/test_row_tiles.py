@@ -10,13 +10,13 @@ ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 MOST_ROWS = 2 ** 31 - 129
 
 # beside every multiple of 32 up to a few tiles, odd sizes, and around where a sum with the tiles' width (2^31 - 255,
-# 2^31 - 191) or with their number (2136356790 and 2139095041) passes 31 bits
+# 2^31 - 191) or with their number (2136356790 and 2139127681) passes 31 bits
 COUNTS = sorted({*(32 * i + j for i in range(1, 60) for j in (-1, 0, 1)), *(7 ** i for i in range(1, 12)),
-                 *(2136356789 + i for i in range(-200, 400)), *(2139095041 + i for i in range(-300, 300)),
+                 *(2136356789 + i for i in range(-200, 400)), *(2139127681 + i for i in range(-300, 300)),
                  *(2 ** 31 - i for i in range(129, 700)), *(2 ** i + j for i in range(11, 31) for j in (-1, 0, 1))})
 
 
-@pytest.mark.parametrize("most", [192])
+@pytest.mark.parametrize("most", [192, 256])
 def test_every_row_is_in_a_tile(tmp_path, most):
     cxx = shutil.which("g++") or shutil.which("c++")
     if cxx is None:

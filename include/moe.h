@@ -779,6 +779,9 @@ typedef struct {
  * [E, N, K], w_scales fp32 [E, N], y bf16 [rows, N]. Any int8 value is taken, -128
  * too. Sums of whole numbers are exact while they and their parts stay within
  * 2^24 in magnitude, and fp32 sums beyond; the two factors are fp32 products.
+ * Few rows are summed in 32-bit integers, exact at any K: with desc.rows at most
+ * 16 and at most 2 E + 4. Past 2^24 a row's last bits may therefore depend on how
+ * many rows the buffers have.
  * A scale that is NaN makes its row or channel NaN. For rows out of RAW records:
  * x = records + off_payload with x_stride = record_bytes, x_scales = records +
  * off_scales with x_scale_stride = record_bytes / 4. x, w and y 16-byte aligned,

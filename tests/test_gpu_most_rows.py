@@ -1,9 +1,10 @@
 """The experts' products with as many rows as they take, 2^31 - 129, nearly all of
-one expert (80 GB): each of them is in a tile and where it belongs."""
+one expert (80 GB): each of them is in a tile and where it belongs. And as many rows
+to 8 bits (110 GB)."""
 import pytest
 import torch
 
-from test_gpu_experts import whole
+from test_gpu_experts import normal, whole
 from test_gpu_experts_i8 import DEV, codes, scales
 from test_gpu_i8_edges import near_swiglu, product_of
 
@@ -17,6 +18,11 @@ def moe():
     from combine_moe_layout_03_gb300 import moe as m
     yield m
     assert m.moe_device_status() == m.MOE_OK
+
+
+@pytest.fixture(autouse=True)
+def memory():
+    yield
     torch.cuda.empty_cache()
 
 
@@ -74,3 +80,20 @@ def test_bf16_products(moe, name):
                    for e, (i, j) in enumerate(zip(b.tolist(), t.tolist()))])
     assert near_swiglu(y[at], v) if "swiglu" in name else torch.equal(y[at], v.to(torch.bfloat16))
     assert rows_that_are_not_zero(y) == rows_that_are_not_zero(y[at])
+
+
+def test_rows_to_8_bits(moe):
+    n = 2 ** 31 - 1
+    at = torch.cat([places(), torch.arange(n - 130, n, device=DEV)]).unique()
+    x = torch.zeros(n, 16, dtype=torch.bfloat16, device=DEV)
+    x[at] = normal(1, len(at), 16)
+    q = torch.full((n, 16), 9, dtype=torch.int8, device=DEV)
+    s = torch.full((n, 1), 9.0, device=DEV)
+    moe.moe_quantize_rows(moe.MoeQuantDesc(n, 16), x, q, s)
+    few = moe.moe_quantize_rows(moe.MoeQuantDesc(len(at), 16), x[at])
+    assert torch.equal(q[at], few[0]) and torch.equal(s[at], few[1])
+    assert rows_that_are_not_zero(q) == len(at)
+    # a row of zeros has the scale of the floor: that of the first row that is zero stands for all
+    zero = moe.moe_quantize_rows(moe.MoeQuantDesc(1, 16), torch.zeros(1, 16, dtype=torch.bfloat16, device=DEV))[1]
+    piece = 1 << 26
+    assert sum(int((s[i:i + piece] == zero).count_nonzero()) for i in range(0, n, piece)) == n - len(at)

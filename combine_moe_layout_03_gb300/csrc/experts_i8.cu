@@ -39,7 +39,7 @@
 // experts of 410 to 614, 7168 -> 2 x 2048, hold 1.4 kW and 1657 of 2070 MHz, 600 to
 // 665 us by GPU (1450 to 1600 TFLOP/s; in bf16 691 to 726 us). 4608 rows in 8
 // experts run at 1720 TFLOP/s in short runs and 1600 in long ones, 12345 uneven
-// rows 2048 -> 7168 at 1370 to 1440 (251 to 265 us).
+// rows 2048 -> 7168 at 1370 to 1440 (248 to 265 us).
 // Few rows: the weights, 256 rows in 32 experts 142 to 149 us (941 MB, 6.3 to 6.6 TB/s).
 #include <mutex>
 
@@ -665,8 +665,10 @@ cudaError_t launch(const ExpertI8Params& p, cudaStream_t s) {
 
 // A few rows go to a kernel that streams the weights, if there are no more than
 // some two for each expert on average: it takes two at a time and reads the
-// weights again (from L2) for more, and tiles take the same time for 1 to 32. The
-// counts of each expert are not known here. (First product 7168 -> 2 x 2048, tiles /
+// weights again (from L2) for more, and tiles take the same time for 1 to 32. What
+// counts is how many rows the buffers have: the counts of each expert are on the
+// device, so 16 rows of one expert among many are streamed, and a few rows in
+// large buffers are not. (First product 7168 -> 2 x 2048, tiles /
 // streamed: 1 row 25 / 7 us, 4 rows of one expert 24 / 12, 8 24 / 19, 16 24 / 35; 8
 // rows in 8 experts 48 / 37, 16 in 16 86 / 74, in 8 48 / 38; 32 in 32 145 / 134, in
 // 8 48 / 70. Second product: 8 rows of one expert 10 / 11 us.)

@@ -12,9 +12,10 @@
 // 12.4 us by one warp each, 7.4 by four).
 //
 // What bounds it: memory. One token's first product (8 experts, 7168 -> 2 x 2048,
-// 235 MB) takes 37.5 us (6.3 TB/s), its second (2048 -> 7168, 117 MB) 19.0. Four
-// blocks an SM, a piece of four rows each way: three or two blocks 42 and 46 us,
-// with a second piece under way 44 to 52 (registers). Whole 512 bytes of a row
+// 235 MB) takes 36.5 to 37.5 us (6.3 to 6.4 TB/s), its second (2048 -> 7168, 117 MB)
+// 18.6 to 19.4. Four blocks an SM, a piece of four rows each way: three or two
+// blocks 42 and 46 us, with a second piece under way 44 to 52 (registers: four
+// blocks leave a thread 64, and 40 bytes of it are in local memory as it is). Whole 512 bytes of a row
 // count: 64 bytes of eight rows at a time, as a matrix product's fragment wants
 // them, came to 47 us, and the integer matrix instruction on them to 45 (it is
 // slow on this chip, 60% busy with one row of eight in use).

@@ -2,11 +2,15 @@
 //
 //   a = max(max_k |x[r, k]|, 1e-30), q[r, k] = rint(x[r, k] * (127 / a)), scale[r] = a / 127
 //
-// Every value is read once: a row stays in the registers of the threads that
-// share it while its largest magnitude is found, and its codes leave from there.
+// Every value is read once: a row stays with the threads that share it while its
+// largest magnitude is found, and its codes leave from there. It stays in their
+// registers, but for fp32 rows of more than 16384 elements: 1024 threads have 64
+// registers each, which eight pieces fill, and 116 bytes of a thread's 256 pass
+// through local memory.
 // What bounds it: memory (32768 x 2048 bf16 30.4 us, 201 MB at 6.6 TB/s; 32768 x
-// 7168 fp32 164 us, 1.17 GB at 7.2 TB/s, more reads than a copy has), and the
-// launch for a few rows (2.4 us).
+// 7168 fp32 164 us, 1.17 GB at 7.2 TB/s, more reads than a copy has; 8192 x 16384
+// fp32 7.0 TB/s, the wider ones 4.5 to 5.0 for 4096 x 32768 and 2048 x 65536), and
+// the launch for a few rows (2.4 us).
 #include "moe_internal.cuh"
 
 namespace moe {

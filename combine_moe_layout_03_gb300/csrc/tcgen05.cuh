@@ -41,7 +41,8 @@ __device__ __forceinline__ void arrive_at(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 // A release to this block alone. To the other block it hands over no memory,
-// only tensor memory that has been read (after tmem_fence_before).
+// only tensor memory that has been read, or written by stores that were waited
+// for (after tmem_fence_before, which orders them before what waits here).
 __device__ __forceinline__ void arrive_local_at(uint32_t bar, uint32_t on) {
   asm volatile(
       "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %1, 0;\n\t@p mbarrier.arrive.shared::cluster.b64 _, [%0];\n\t}" ::"r"(bar),
